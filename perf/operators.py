@@ -224,7 +224,7 @@ def _plain_append(s):
     for x_, pages, scales in ((_rotate(x[:, h:h + hkv], cos, sin, case["pairs"]), s["k_pages"], s["k_scales"]),
                               (x[:, h + hkv:], s["v_pages"], s["v_scales"])):
         amax = torch.zeros_like(scales).index_reduce_(0, page, x_.abs().amax(-1), "amax")
-        m, e = torch.frexp(amax)
+        m, e = torch.frexp(amax.clamp(min=2.0 ** -120))
         need = torch.ldexp(torch.ones_like(m), (e - 9 + (m > 0.875).int()).clamp(-120, 120))
         was = scales[first]
         now = torch.where(part, torch.maximum(was, need[first]), was)
@@ -367,7 +367,7 @@ def exact(case, seed):
                 page = table[b][p]
                 for c in range(2):
                     piece = rows[lo - o:hi - o, h + c * hkv:h + (c + 1) * hkv]
-                    m, e = torch.frexp(piece.abs().amax((0, 2)))
+                    m, e = torch.frexp(piece.abs().amax((0, 2)).clamp(min=2.0 ** -120))
                     now = torch.ldexp(torch.ones_like(m), (e - 9 + (m > 0.875).int()).clamp(-120, 120))
                     if lo > p * ps:
                         now = torch.maximum(now, scale[c][page])
