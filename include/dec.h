@@ -309,6 +309,121 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
                           int32_t n_kv_heads, int32_t head_dim, int32_t n_pos, int32_t cache_stride, float* out,
                           void* stream);
 
+/* ------------------------------------------- operators on packed sequences
+ *
+ * Three operators for callers that hold several sequences, or their own prompt:
+ * dec_attention_prefill (attention of whole prompts), dec_kv_append (position
+ * rotation, and keys and values into a paged 8-bit cache) and dec_attention_paged
+ * (one query token a sequence over that cache).  The pages have no counterpart of
+ * them.  Like dec_attention_noalloc they need no context, allocate nothing, run
+ * asynchronously on `stream` (a cudaStream_t of the current device, NULL = the
+ * legacy default stream), can be captured into a CUDA graph, and return
+ * DEC_ERR_CUDA without launching while a CUDA error of an earlier runtime call of
+ * this library is pending.  All pointers except the structs' own are device
+ * pointers of the current device; a pointer of the host or of another device, or
+ * one that breaks its alignment, returns INVALID_ARG before anything runs.  Row
+ * strides are counted in elements, from one token's first head to the next
+ * token's; a token's heads lie one behind the other.
+ *
+ * dtype: DEC_BF16 or DEC_F32, the type of q, k, v and out.  Sums, softmax
+ * statistics and rotations are fp32 or better; results are rounded once.
+ * Limits (DEC_ERR_UNSUPPORTED otherwise): head_dim 64 or 128, n_heads a multiple of
+ * n_kv_heads with at most 8 query heads per kv head (query head h reads kv head
+ * h / (n_heads / n_kv_heads)).
+ *
+ * Offsets, lengths and page tables live on the device, so a captured graph can be
+ * replayed on other sequences.  A host call cannot refuse what they hold: a
+ * sequence whose entry is inconsistent is skipped, never read or written out of
+ * range, and DEC_SEQ_* bits are OR-ed into *status (device int32, nullable; the
+ * caller zeroes it). */
+#define DEC_SEQ_BAD_PAGE 1  /* a page id below 0 or >= n_pages: its positions are left out */
+#define DEC_SEQ_BAD_RANGE 2 /* offsets decreasing, outside the rows given or above the given maximum, or a length
+                               that is negative, shorter than its new tokens or longer than its table row: the
+                               sequence is left out (attention: its output rows are zeroed where they are known) */
+
+#define DEC_ROPE_HALF 0      /* pairs (j, j + rot_dim/2) */
+#define DEC_ROPE_NEIGHBOUR 1 /* pairs (2j, 2j + 1) */
+
+/* Keys and values in pages of page_size positions, E4M3, one scale for each (page,
+ * kv head) of K and of V: value = code * scale.  The scales are powers of two, so
+ * no precision beyond E4M3's is lost when one grows.  Position t of sequence s is
+ * row t % page_size of page page_table[s * table_stride + t / page_size].  The
+ * caller owns the memory and hands out the pages; pages that only readers use
+ * (a shared prefix) may stand in several rows of the table. */
+typedef struct dec_paged_cache {
+  void* k_pages;   /* [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned */
+  void* v_pages;   /* same */
+  float* k_scales; /* [n_pages][n_kv_heads] */
+  float* v_scales; /* same */
+  int32_t n_pages, page_size, n_kv_heads, head_dim; /* page_size 16, 32, 64 or 128 */
+} dec_paged_cache;
+
+/* The rotation: dims below rot_dim, by angle position * inv_freq[j] for pair j
+ * (evaluated in fp64, so far positions keep their angle); cos and sin are
+ * multiplied by factor.  Every scaling for long contexts is a choice of inv_freq and
+ * factor.  rot_dim 0: no rotation (inv_freq may be NULL). */
+typedef struct dec_rope {
+  const double* inv_freq; /* device [rot_dim / 2] */
+  int32_t rot_dim;        /* a multiple of 16, at most head_dim */
+  int32_t pairs;          /* DEC_ROPE_HALF | DEC_ROPE_NEIGHBOUR */
+  float factor;           /* 1 unless the scaling asks for another */
+} dec_rope;
+
+/* Append the new tokens of n_seqs sequences.  Sequence s owns rows cu_new[s] ..
+ * cu_new[s + 1] - 1 of q, k and v (none: nothing to do); seq_lens[s] is its length
+ * AFTER the append, so its first new token has position seq_lens[s] - (its rows).
+ *   - q (nullable) is rotated into q_out (the same buffer and stride: in place);
+ *   - k is rotated, k and v are stored.  The scale of a page that starts with this
+ *     call is the smallest power of two 2^e, -120 <= e <= 120, with max|x| <= 448 * 2^e
+ *     over the page's new finite values; a page that already holds rows of the sequence
+ *     keeps its scale, or gets that larger one, its earlier rows being rounded again
+ *     to E4M3 (exact but for codes that become subnormal).  Values round to nearest
+ *     even; infinities saturate; NaN is stored as NaN.
+ * Rows behind the last sequence's last row, and page rows that hold no position
+ * written here or before, stay as they are.  A page that is written may belong to
+ * one sequence of the call only.
+ *   q, k, v, q_out  16-byte aligned, row strides multiples of 16 bytes
+ *   max_new         at least the largest number of new tokens of a sequence
+ *   n_tokens        rows of q, k and v
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int dec_kv_append(const dec_paged_cache* cache, const dec_rope* rope, int32_t dtype, const void* q, const void* k,
+                  const void* v, void* q_out, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                  int64_t q_out_stride, int32_t n_heads, int32_t n_seqs, int32_t n_tokens, int32_t max_new,
+                  const int32_t* cu_new, const int32_t* seq_lens, const int32_t* page_table, int32_t table_stride,
+                  int32_t* status, void* stream);
+
+/* Bytes of workspace that dec_attention_paged needs for these sizes, on any device.
+ * Errors: INVALID_ARG, UNSUPPORTED. */
+int dec_attention_paged_workspace(const dec_paged_cache* cache, int32_t n_seqs, int32_t n_heads, size_t* out_bytes);
+
+/* Attention of one query token a sequence over its seq_lens[s] cached positions:
+ * out[s][h] = softmax_t(scale * q[s][h] . K[t]) V[t], t < seq_lens[s]; zeros for an
+ * empty sequence.  What the pages hold behind the length is never used.
+ *   q, out     [n_seqs] rows, 16-byte aligned, strides multiples of 16 bytes
+ *   workspace  dec_attention_paged_workspace bytes, 16-byte aligned, nothing to be initialised;
+ *              calls that may overlap on the GPU need one each
+ * Errors: INVALID_ARG (scale not finite and positive, workspace too small, ...), UNSUPPORTED, CUDA. */
+int dec_attention_paged(const dec_paged_cache* cache, int32_t dtype, const void* q, void* out, int64_t q_stride,
+                        int64_t out_stride, int32_t n_heads, int32_t n_seqs, const int32_t* seq_lens,
+                        const int32_t* page_table, int32_t table_stride, float scale, void* workspace,
+                        size_t workspace_bytes, int32_t* status, void* stream);
+
+/* Attention of packed prompts.  Sequence s has query rows cu_q[s] .. cu_q[s + 1] - 1
+ * and key rows cu_k[s] .. cu_k[s + 1] - 1 (as many, or more: a later chunk of a prompt
+ * whose earlier keys are given too).  causal != 0: the last query sees every key, the
+ * one before it one fewer, and so on; a query that sees no key gets zeros.
+ *   out[i][h] = softmax_t(scale * q[i][h] . k[t]) v[t]
+ * Keys and values that a query does not see do not touch its result, whatever they
+ * hold.  Rows of out behind the last sequence stay as they are.
+ *   q, k, v, out  16-byte aligned, row strides multiples of 16 bytes
+ *   n_q, n_k      rows of q (and out) and of k and v;  max_q: at least the longest query range
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int dec_attention_prefill(int32_t dtype, const void* q, const void* k, const void* v, void* out, int64_t q_stride,
+                          int64_t k_stride, int64_t v_stride, int64_t out_stride, int32_t n_heads, int32_t n_kv_heads,
+                          int32_t head_dim, int32_t n_seqs, int32_t n_q, int32_t n_k, int32_t max_q,
+                          const int32_t* cu_q, const int32_t* cu_k, int32_t causal, float scale, int32_t* status,
+                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif

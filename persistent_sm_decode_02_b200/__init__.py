@@ -5,4 +5,5 @@ kernels of libdec.so.  Importing this package loads the library and fails
 loudly if it has not been built (there is no CPU fallback).
 """
 from .dec import *  # noqa: F401,F403
-from .dec import LIB_PATH, DecError, Decoder, config_from_workload, load_library  # noqa: F401
+from .dec import (LIB_PATH, DecError, Decoder, PagedCache, attention_prefill, config_from_workload,  # noqa: F401
+                  load_library)

@@ -39,6 +39,11 @@ DEC_W = dict(embed=1, final_norm=2, lm_head=3, attn_norm=10, wq=11, wk=12, wv=13
              w_gate=16, w_up=17, w_down=18, q_a=20, q_a_norm=21, q_b=22, kv_a=23, kv_a_norm=24, kv_b=25,
              router=30, exp_gate=31, exp_up=32, exp_down=33, sh_gate=34, sh_up=35, sh_down=36)
 
+DEC_SEQ_BAD_PAGE = 1
+DEC_SEQ_BAD_RANGE = 2
+DEC_ROPE_HALF = 0
+DEC_ROPE_NEIGHBOUR = 1
+
 DEC_DUMP_KV = 1
 DEC_DUMP_ROUTES = 2
 DEC_DUMP_TRACE = 3
@@ -51,7 +56,8 @@ DEC_DUMP_OP = 100
 EXPORTED = ["dec_create", "dec_load_weights", "dec_set_kv_cache", "dec_step", "dec_step_async", "dec_sync",
             "dec_reset", "dec_destroy", "dec_set_stream", "dec_set_exec_mode", "dec_position", "dec_debug_dump",
             "dec_last_error", "dec_attention_noalloc", "dec_generate_async", "dec_generate_poll",
-            "dec_generate_stop", "dec_generate_wait", "dec_generate"]
+            "dec_generate_stop", "dec_generate_wait", "dec_generate", "dec_kv_append", "dec_attention_paged_workspace",
+            "dec_attention_paged", "dec_attention_prefill"]
 
 
 class dec_config(ctypes.Structure):
@@ -69,6 +75,17 @@ class dec_tensor(ctypes.Structure):
                 ("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("bytes", ctypes.c_size_t)]
 
 
+class dec_paged_cache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class dec_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("pairs", ctypes.c_int32),
+                ("factor", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -79,7 +96,7 @@ def load_library():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with __graft_entry__.build(); "
                                "this package has no CPU fallback")
         L = ctypes.CDLL(LIB_PATH)
-        P = ctypes.c_void_p
+        P, I, LL = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
         sig = {
             "dec_create": [ctypes.POINTER(dec_config), ctypes.POINTER(P)],
             "dec_load_weights": [P, ctypes.POINTER(dec_tensor), ctypes.c_int],
@@ -100,6 +117,12 @@ def load_library():
             "dec_generate_stop": [P],
             "dec_generate_wait": [P, P, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
             "dec_generate": [P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, ctypes.POINTER(ctypes.c_int32)],
+            "dec_kv_append": [ctypes.POINTER(dec_paged_cache), ctypes.POINTER(dec_rope), I] + [P] * 4 + [LL] * 4
+            + [I] * 4 + [P] * 3 + [I, P, P],
+            "dec_attention_paged_workspace": [ctypes.POINTER(dec_paged_cache), I, I, ctypes.POINTER(ctypes.c_size_t)],
+            "dec_attention_paged": [ctypes.POINTER(dec_paged_cache), I, P, P, LL, LL, I, I, P, P, I, ctypes.c_float,
+                                    P, ctypes.c_size_t, P, P],
+            "dec_attention_prefill": [I] + [P] * 4 + [LL] * 4 + [I] * 7 + [P, P, I, ctypes.c_float, P, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -203,6 +226,34 @@ def dec_generate_wait(ctx, out_tokens, cap, out_count):
 
 def dec_generate(ctx, token_id, n_steps, stop_token, out_tokens, out_count):
     return load_library().dec_generate(ctx, token_id, n_steps, stop_token, out_tokens, out_count)
+
+
+def dec_kv_append(cache, rope, dtype, q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride, n_heads, n_seqs,
+                  n_tokens, max_new, cu_new, seq_lens, page_table, table_stride, status, stream):
+    """Rotate and append new tokens to a paged 8-bit cache (device addresses in, status code out); see include/dec.h."""
+    return load_library().dec_kv_append(cache, rope, dtype, q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride,
+                                        n_heads, n_seqs, n_tokens, max_new, cu_new, seq_lens, page_table,
+                                        table_stride, status, stream)
+
+
+def dec_attention_paged_workspace(cache, n_seqs, n_heads, out_bytes):
+    return load_library().dec_attention_paged_workspace(cache, n_seqs, n_heads, out_bytes)
+
+
+def dec_attention_paged(cache, dtype, q, out, q_stride, out_stride, n_heads, n_seqs, seq_lens, page_table, table_stride,
+                        scale, workspace, workspace_bytes, status, stream):
+    """One query token a sequence over a paged 8-bit cache (device addresses in, status code out); see include/dec.h."""
+    return load_library().dec_attention_paged(cache, dtype, q, out, q_stride, out_stride, n_heads, n_seqs, seq_lens,
+                                              page_table, table_stride, scale, workspace, workspace_bytes, status,
+                                              stream)
+
+
+def dec_attention_prefill(dtype, q, k, v, out, q_stride, k_stride, v_stride, out_stride, n_heads, n_kv_heads, head_dim,
+                          n_seqs, n_q, n_k, max_q, cu_q, cu_k, causal, scale, status, stream):
+    """Attention of packed prompts (device addresses in, status code out); see include/dec.h."""
+    return load_library().dec_attention_prefill(dtype, q, k, v, out, q_stride, k_stride, v_stride, out_stride, n_heads,
+                                                n_kv_heads, head_dim, n_seqs, n_q, n_k, max_q, cu_q, cu_k, causal,
+                                                scale, status, stream)
 
 
 # ---- convenience
@@ -319,3 +370,60 @@ class Decoder:
 
     def plan_text(self) -> str:
         return self.dump(DEC_DUMP_PLAN).rstrip(b"\0").decode()
+
+
+_ERR_TEXT = {DEC_ERR_INVALID_ARG: "bad pointer, size, stride or enum value", DEC_ERR_CUDA: "a CUDA call failed",
+             DEC_ERR_UNSUPPORTED: "sizes outside what the kernels implement"}
+
+
+def _chk_op(name, rc):
+    if rc != DEC_OK:
+        raise DecError(rc, f"{name}: {_ERR_TEXT.get(rc, 'error')}")
+
+
+class PagedCache:
+    """A paged 8-bit key/value cache in the caller's memory (device addresses; layout in include/dec.h), with the
+    operators on it.  Strides are in elements and default to contiguous [rows][heads][head_dim]; scale defaults to
+    1/sqrt(head_dim); stream is a cudaStream_t (None: the legacy default stream)."""
+
+    def __init__(self, k_pages, v_pages, k_scales, v_scales, *, n_pages, page_size, n_kv_heads, head_dim):
+        self.c = dec_paged_cache(k_pages, v_pages, k_scales, v_scales, n_pages, page_size, n_kv_heads, head_dim)
+
+    def append(self, q, k, v, q_out, cu_new, seq_lens, page_table, *, table_stride, n_seqs, n_tokens, max_new, n_heads,
+               dtype=DEC_BF16, strides=None, inv_freq=None, rot_dim=0, neighbour_pairs=False, factor=1.0, status=None,
+               stream=None):
+        """dec_kv_append; strides: (q, k, v, q_out).  q and q_out may be None: keys and values alone."""
+        if strides is None:
+            row, kv = n_heads * self.c.head_dim, self.c.n_kv_heads * self.c.head_dim
+            strides = (row, kv, kv, row)
+        rope = dec_rope(inv_freq, rot_dim, DEC_ROPE_NEIGHBOUR if neighbour_pairs else DEC_ROPE_HALF, factor)
+        _chk_op("dec_kv_append", dec_kv_append(self.c, rope, dtype, q, k, v, q_out, *strides, n_heads, n_seqs, n_tokens,
+                                               max_new, cu_new, seq_lens, page_table, table_stride, status, stream))
+
+    def workspace_bytes(self, n_seqs, n_heads) -> int:
+        n = ctypes.c_size_t(0)
+        _chk_op("dec_attention_paged_workspace",
+                dec_attention_paged_workspace(self.c, n_seqs, n_heads, ctypes.byref(n)))
+        return n.value
+
+    def attention(self, q, out, seq_lens, page_table, *, table_stride, n_seqs, n_heads, workspace, workspace_bytes,
+                  dtype=DEC_BF16, q_stride=None, out_stride=None, scale=None, status=None, stream=None):
+        """dec_attention_paged."""
+        row = n_heads * self.c.head_dim
+        _chk_op("dec_attention_paged",
+                dec_attention_paged(self.c, dtype, q, out, row if q_stride is None else q_stride,
+                                    row if out_stride is None else out_stride, n_heads, n_seqs, seq_lens, page_table,
+                                    table_stride, self.c.head_dim ** -0.5 if scale is None else scale, workspace,
+                                    workspace_bytes, status, stream))
+
+
+def attention_prefill(q, k, v, out, cu_q, cu_k, *, n_seqs, n_q, n_k, max_q, n_heads, n_kv_heads, head_dim,
+                      dtype=DEC_BF16, causal=True, strides=None, scale=None, status=None, stream=None):
+    """dec_attention_prefill; strides (q, k, v, out) in elements, contiguous [rows][heads][head_dim] by default;
+    scale defaults to 1/sqrt(head_dim)."""
+    if strides is None:
+        strides = (n_heads * head_dim, n_kv_heads * head_dim, n_kv_heads * head_dim, n_heads * head_dim)
+    _chk_op("dec_attention_prefill",
+            dec_attention_prefill(dtype, q, k, v, out, *strides, n_heads, n_kv_heads, head_dim, n_seqs, n_q, n_k, max_q,
+                                  cu_q, cu_k, int(causal), head_dim ** -0.5 if scale is None else scale, status,
+                                  stream))
