@@ -340,6 +340,7 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
 #define DEC_SEQ_BAD_RANGE 2 /* offsets decreasing, outside the rows given or above the given maximum, or a length
                                that is negative, shorter than its new tokens or longer than its table row: the
                                sequence is left out (attention: its output rows are zeroed where they are known) */
+#define DEC_SEQ_TIMEOUT 4   /* a wait inside a kernel ran out (a second; never expected): results are incomplete */
 
 #define DEC_ROPE_HALF 0      /* pairs (j, j + rot_dim/2) */
 #define DEC_ROPE_NEIGHBOUR 1 /* pairs (2j, 2j + 1) */

@@ -1,36 +1,10 @@
 // dec_attention_prefill: attention of packed prompts.
 #include "op_common.cuh"
+#include "prefill_tc.cuh"
 
 namespace {
 
 using namespace dec_op;
-
-struct PrefillArgs {
-  const void *q, *k, *v;
-  void* out;
-  int64_t qs, ks, vs, os;
-  int heads, gs, n_q, n_k, max_q, causal;
-  const int32_t *cu_q, *cu_k;
-  float scale_log2;
-  int32_t* status;
-};
-
-struct Range {
-  int64_t q0, k0;
-  int lq, lk;
-  bool ok;
-};
-__device__ __forceinline__ Range range_of(const PrefillArgs& a, int s) {
-  const int64_t q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
-  const bool q_ok = q0 >= 0 && q1 >= q0 && q1 <= a.n_q, k_ok = k0 >= 0 && k1 >= k0 && k1 <= a.n_k;
-  Range r;
-  r.q0 = q0;
-  r.k0 = k_ok ? k0 : 0;
-  r.lq = q_ok ? (int)(q1 - q0) : 0;
-  r.lk = k_ok ? (int)(k1 - k0) : 0;
-  r.ok = q_ok && k_ok && r.lq <= a.max_q;
-  return r;
-}
 
 // One block per (64 queries, head): scores and values on the CUDA cores in fp32, 4 x 4 scores and 4 x (D / 16)
 // outputs a thread, 64 keys at a time with the running maximum and sum of the softmax.
@@ -176,7 +150,7 @@ extern "C" int dec_attention_prefill(int32_t dtype, const void* q, const void* k
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == DEC_BF16)
-    e = D == 64 ? launch_simt<__nv_bfloat16, 64>(a, n_seqs, st) : launch_simt<__nv_bfloat16, 128>(a, n_seqs, st);
+    e = D == 64 ? tc::launch<64>(a, n_seqs, st) : tc::launch<128>(a, n_seqs, st);
   else
     e = D == 64 ? launch_simt<float, 64>(a, n_seqs, st) : launch_simt<float, 128>(a, n_seqs, st);
   return e == cudaSuccess ? DEC_OK : DEC_ERR_CUDA;

@@ -41,6 +41,7 @@ DEC_W = dict(embed=1, final_norm=2, lm_head=3, attn_norm=10, wq=11, wk=12, wv=13
 
 DEC_SEQ_BAD_PAGE = 1
 DEC_SEQ_BAD_RANGE = 2
+DEC_SEQ_TIMEOUT = 4
 DEC_ROPE_HALF = 0
 DEC_ROPE_NEIGHBOUR = 1
 
