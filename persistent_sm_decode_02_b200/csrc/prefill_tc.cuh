@@ -1,15 +1,16 @@
 // Attention of packed bf16 prompts on tcgen05 tensor cores.
 //
-// A block takes 256 queries of one head as two tiles of 128, and walks their keys 128 at a time:
-//   S = Q K^T (128 x 128, fp32 in TMEM), P = 2^(scale log2(e) S - m) rounded to bf16 over S, O += P V.
-// Warps 0-3 and 4-7 are the tiles' softmax, a thread a row; warp 8 issues every MMA; warp 9 every TMA load.  The softmax
-// keeps a row of S in registers: it takes them over from the last warpgroup (208 and 88 of the 168 at launch).
-// The tiles alternate: while one tile's softmax runs, the tensor cores do the other's P V and next Q K^T.
-//   TMEM: S0 | S1 (128 columns each, P in their first 64) | O0 | O1 (D columns each)
+// A block takes two tiles of 128 queries that read the same keys (two heads of one kv head, or neighbouring queries
+// of one head), and walks their keys 64 at a time:
+//   S = Q K^T (128 x 64, fp32 in TMEM), P = 2^(scale log2(e) S - m) rounded to bf16 over S, O += P V.
+// Warps 0-3 and 4-7 are the tiles' softmax, a thread a row; warp 8 issues every MMA; warp 9 every TMA load.
+//   TMEM: S of tile 0, two buffers of 64 columns (P in the first 32 of each) | S of tile 1 | O0 | O1 (D columns each)
 //   shared memory: Q, and a ring of K and V tiles, rows of 128 bytes in the 128-byte swizzle
-// One thread's MMAs complete in the order they were issued.  So S_i(j + 1), issued behind P V_i(j), may overwrite P_i(j),
-// and once it has arrived O_i is at rest until the tile's next P: a softmax thread may rescale its row of O there, with
-// no other barrier.  It does only when the row's maximum has grown by more than 2^8 (P up to 2^8 and its sum lose nothing).
+// Each tile has the scores of two steps in TMEM, so its softmax goes from one step to the next while the tensor cores
+// do P V of the step before and Q K^T of the one after: neither waits for the other's latency.
+// One thread's MMAs complete in the order they were issued, so S_i(j + 2), issued behind P V_i(j), may overwrite P_i(j).
+// A row of O is rescaled only when the row's maximum has grown by more than 2^8 (P up to 2^8 and its sum lose
+// nothing); the softmax thread then waits for P V of the step before and does it in TMEM.
 //
 // P is rounded to bf16 (2^-9 of each weight, of the same size as V's own rounding and the result's); its sum is
 // of the unrounded weights, in fp32.
@@ -19,6 +20,8 @@
 // it sees alone (redo_row).
 #pragma once
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "op_common.cuh"
 #include "ptx.cuh"
@@ -60,20 +63,39 @@ using dec::smem_u32;
 
 constexpr int kThreads = 384, kRegs = 168, kRegsSoftmax = 208, kRegsRest = 88;
 static_assert(256 * kRegsSoftmax + 128 * kRegsRest <= kThreads * kRegs, "registers handed over are those at launch");
-constexpr int kM = 128, kN = 128;
+constexpr int kM = 128;
+#ifndef KPOLY
+#define KPOLY 2
+#endif
+constexpr int kPoly = KPOLY;  // of every 8 pairs of a row, those whose exponentials are the polynomial's
+constexpr float kC0 = 0x1.fff692p-1f, kC1 = 0x1.62f31ap-1f, kC2 = 0x1.f0de1ap-3f, kC3 = 0x1.c3f75ep-5f;
 
 template <int D>
 struct Shape {
-  static constexpr int kStages = D == 128 ? 4 : 8;
-  static constexpr int kTile = 128 * D * 2;  // bytes of 128 rows
-  static constexpr int kSmem = (2 + kStages) * kTile + 1024;  // more than half an SM's: one block, and its 512 TMEM columns, per SM
+#ifndef KN128
+#define KN128 128
+#define KN64 128
+#endif
+  static constexpr int kN = D == 128 ? KN128 : KN64;      // keys of a step
+  static constexpr int kBufs = kN == 128 ? 1 : 2;   // steps whose scores a tile has in TMEM
+  static constexpr int kStages = (D == 128 ? 128 : 96) * 1024 / (kN * D * 2);
+  static constexpr int kQ = kM * D * 2, kTile = kN * D * 2;  // bytes of a query tile, of a step's keys or values
+  static constexpr int kSmem = 2 * kQ + kStages * kTile + 512;  // barriers behind the tiles;  // over half an SM's: one block, and its 512 TMEM columns, per SM
 };
 
 struct Bars {
-  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], drained;
+  uint64_t q_full, kv_full[12], kv_empty[12], s_full[2][2], p_full[2][2], pv_done[2], drained;
   uint32_t tmem;
   int dead;
 };
+
+// One lane of a converged warp.  (Under `lane == 0` the compiler takes the branch for divergent and moves every operand
+// of an MMA to the uniform registers by itself: issuing then took longer than the MMAs.)
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 
 __device__ __forceinline__ uint64_t now_ns() { return dec::globaltimer(); }
 
@@ -131,6 +153,50 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Two fp32 values in a register pair.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 un2(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// (2^x, 2^y) without the special function unit: x = n + f with n the nearest integer (adding 1.5 * 2^23 leaves n in
+// the low bits), 2^f on +-1/2 by the cubic of least relative error (7.5e-5, a 50th of P's rounding to bf16), and n
+// added to the exponent.  Below 2^-126 the result stays there.  A NaN gives a number above bf16's range.
+__device__ __forceinline__ F2 exp2_poly(F2 v) {
+  const float2 u = un2(v);
+  const F2 x = f2(max_nan(u.x, -126.f), max_nan(u.y, -126.f));
+  const F2 t = add2(x, f2(12582912.f, 12582912.f));
+  const F2 f = fma2(add2(t, f2(-12582912.f, -12582912.f)), f2(-1.f, -1.f), x);
+  F2 p = fma2(f, f2(kC3, kC3), f2(kC2, kC2));
+  p = fma2(p, f, f2(kC1, kC1));
+  p = fma2(p, f, f2(kC0, kC0));
+  const float2 a = un2(t), b = un2(p);
+  return f2(__int_as_float(__float_as_int(b.x) + (__float_as_int(a.x) << 23)),
+            __int_as_float(__float_as_int(b.y) + (__float_as_int(a.y) << 23)));
+}
+
 // One row over the `n` keys it sees, on a warp: lanes take keys for the scores and dims for the values.
 template <int D>
 __device__ __forceinline__ void redo_row(const PrefillArgs& a, const __nv_bfloat16* q, const __nv_bfloat16* k,
@@ -170,38 +236,37 @@ __device__ __forceinline__ void redo_row(const PrefillArgs& a, const __nv_bfloat
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                   const __grid_constant__ CUtensorMap v_map, const PrefillArgs a, const int n_seqs) {
+                   const __grid_constant__ CUtensorMap v_map, const PrefillArgs a, const int n_seqs, const int pair) {
   using Sh = Shape<D>;
   using bf16 = __nv_bfloat16;
-  constexpr int kSlabs = D / 64, kSlab = 128 * 128;
+  constexpr int kN = Sh::kN, kBufs = Sh::kBufs, kSlabs = D / 64, kRow = 128;  // slabs of 64 elements: rows of 128 bytes
   constexpr uint32_t kIdS = dec::umma_idesc_bf16(kM, kN, false), kIdO = dec::umma_idesc_bf16(kM, D, true);
-  extern __shared__ uint8_t raw[];
-  __shared__ Bars b;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  Bars& b = *reinterpret_cast<Bars*>(sm + 2 * Sh::kQ + Sh::kStages * Sh::kTile);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int head = blockIdx.x % a.heads, s = blockIdx.x / a.heads % n_seqs;
-  const int tile = gridDim.x / a.heads / n_seqs - 1 - blockIdx.x / a.heads / n_seqs;  // long rows first
+  // pair: the tiles are heads 2x and 2x + 1; else queries m0 and m0 + 128
+  const int columns = pair ? a.heads / 2 : a.heads;
+  const int head0 = (pair ? 2 : 1) * (blockIdx.x % columns), s = blockIdx.x / columns % n_seqs;
+  const int tile = gridDim.x / columns / n_seqs - 1 - blockIdx.x / columns / n_seqs;  // long rows first
   const Range r = range_of(a, s);
   if (!r.ok && tid == 0) flag(a.status, DEC_SEQ_BAD_RANGE);
-  const int m0 = tile * 2 * kM, kvh = head / a.gs, shift = r.lk - r.lq;
+  const int m0 = tile * (pair ? kM : 2 * kM), mstep = pair ? 0 : kM, kvh = head0 / a.gs, shift = r.lk - r.lq;
   if (m0 >= r.lq) return;
-  // 128-key steps of each tile, up to the last key its last row sees
-  int n[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int mi = m0 + i * kM;
+  // steps of a tile, up to the last key its last row sees
+  auto steps = [&](int i) {
+    const int mi = m0 + i * mstep;
     const int keys = !r.ok || mi >= r.lq ? 0 : a.causal ? min(r.lk, min(mi + kM, r.lq) + shift) : r.lk;
-    n[i] = keys > 0 ? (keys + kN - 1) / kN : 0;
-  }
-  const int n_max = max(n[0], n[1]);
+    return keys > 0 ? (keys + kN - 1) / kN : 0;
+  };
+  const int n0 = steps(0), n1 = steps(1), n_max = max(n0, n1);
 
-  uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* ring = sm + 2 * Sh::kQ;
   if (tid == 0) {
     dec::mbar_init(&b.q_full, 1);
     for (int i = 0; i < Sh::kStages; ++i) dec::mbar_init(&b.kv_full[i], 1), dec::mbar_init(&b.kv_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      dec::mbar_init(&b.s_full[i], 1);
-      dec::mbar_init(&b.p_full[i], kM);
-      dec::mbar_init(&b.o_full[i], 1);
+      for (int k = 0; k < 2; ++k) dec::mbar_init(&b.s_full[i][k], 1), dec::mbar_init(&b.p_full[i][k], kM);
+      dec::mbar_init(&b.pv_done[i], 1);
     }
     dec::mbar_init(&b.drained, 1);
     b.dead = 0;
@@ -214,40 +279,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   dec::tc_fence_before();
   __syncthreads();
   dec::tc_fence_after();
-  const uint32_t tm = b.tmem;
-  const uint32_t tS[2] = {tm, tm + kN}, tO[2] = {tm + 2 * kN, tm + 2 * kN + D};
+  constexpr uint32_t tm = 0;  // all 512 columns are this block's
+  auto tS = [&](int i, int j) { return tm + (i * kBufs + j % kBufs) * kN; };
+  auto tO = [&](int i) { return tm + 256 + i * D; };
+  // place in the order of loads: kBufs of K, then V0 and the next K, V1 and the next ...
+  auto k_at = [&](int j) { return j < kBufs ? j : 2 * j - kBufs + 1; };
+  auto v_at = [&](int j) { return min(2 * j + kBufs, n_max + j); };
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    // ---- softmax of tile i, row m0 + 128 i + (tid & 127)
-    const int i = warp >> 2, row = m0 + i * kM + (tid & 127);
+    // ---- softmax of tile i, one row a thread
+    const int i = warp >> 2, row = m0 + i * mstep + (tid & 127), n = i ? n1 : n0, head = head0 + (pair ? i : 0);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const int end = !r.ok ? 0 : a.causal ? min(r.lk, row + shift + 1) : r.lk;  // keys the row sees
     const int warp_end = __shfl_sync(0xffffffffu, end, 0);  // the fewest in the warp
     const float sl = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < n[i] && ok; ++j) {
-      ok = __all_sync(0xffffffffu, wait(&b.s_full[i], j & 1, &b.dead));
+    for (int j = 0; j < n; ++j) {
+      ok = __all_sync(0xffffffffu, wait(&b.s_full[i][j % kBufs], (j / kBufs) & 1, &b.dead));
       if (!ok) break;
       dec::tc_fence_after();
-      uint32_t x[4][32];
+      uint32_t x[kN / 32][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) dec::tmem_ld32(tS[i] + lanes + c * 32, x[c]);
+      for (int c = 0; c < kN / 32; ++c) dec::tmem_ld32(tS(i, j) + lanes + c * 32, x[c]);
       dec::tmem_wait_ld();
-      float mx = -INFINITY;
-      if (j * kN + kN > warp_end) {
+      const bool masked = j * kN + kN > warp_end;
+      if (masked) {
         const int lim = end - j * kN;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e >= lim) x[c][e] = 0xFF800000u;
+        for (int e = 0; e < kN; ++e)
+          if (e >= lim) x[e / 32][e % 32] = 0xFF800000u;
       }
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
+      for (int e = 0; e < kN; e += 2)
+        mx4[e / 2 % 4] = fmaxf(mx4[e / 2 % 4], fmaxf(__uint_as_float(x[e / 32][e % 32]), __uint_as_float(x[e / 32][e % 32 + 1])));
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       const bool grow = (mx - m) * sl > 8.f || (m == -INFINITY && mx > m);
       if (__any_sync(0xffffffffu, grow)) {
         const float mn = grow ? mx : m;
@@ -255,41 +323,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= f;
         m = mn;
         if (j > 0) {
+          // (S(j) was issued behind P V of step j - 2, so this phase is the one after that)
+          ok = __all_sync(0xffffffffu, wait(&b.pv_done[i], (j - 1) & 1, &b.dead));
+          if (!ok) break;
+          dec::tc_fence_after();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
-            dec::tmem_ld32(tO[i] + lanes + c * 32, o);
+            dec::tmem_ld32(tO(i) + lanes + c * 32, o);
             dec::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(tO[i] + lanes + c * 32, o);
+            tmem_st32(tO(i) + lanes + c * 32, o);
           }
         }
       }
       const float base = m == -INFINITY ? 0.f : m * sl;
-      float sum0 = 0.f, sum1 = 0.f;
+      const F2 sl2 = f2(sl, sl), base2 = f2(-base, -base);
+      F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+      auto weights = [&](auto poly) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t p[32];
+        for (int c = 0; c < kN / 64; ++c) {
+          uint32_t p[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float p0 = dec::ex2_approx(fmaf(__uint_as_float(x[2 * c + e / 16][2 * (e % 16)]), sl, -base));
-          const float p1 = dec::ex2_approx(fmaf(__uint_as_float(x[2 * c + e / 16][2 * (e % 16) + 1]), sl, -base));
-          sum0 += p0;
-          sum1 += p1;
-          const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-          p[e] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int e = 0; e < 32; ++e) {
+            F2 y = f2(__uint_as_float(x[2 * c + e / 16][2 * (e % 16)]), __uint_as_float(x[2 * c + e / 16][2 * (e % 16) + 1]));
+            y = fma2(y, sl2, base2);
+            if (e % 8 < decltype(poly)::value) {
+              y = exp2_poly(y);
+            } else {
+              const float2 u = un2(y);
+              y = f2(dec::ex2_approx(u.x), dec::ex2_approx(u.y));
+            }
+            sum[e & 1] = add2(sum[e & 1], y);
+            const float2 u = un2(y);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(u.x, u.y);
+            p[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st32(tS(i, j) + lanes + c * 32, p);
         }
-        tmem_st32(tS[i] + lanes + c * 32, p);
-      }
-      l += sum0 + sum1;
+      };
+      if (masked)  // an unseen key's weight is exactly zero
+        weights(std::integral_constant<int, 0>());
+      else
+        weights(std::integral_constant<int, kPoly>());
+      const float2 sums = un2(add2(sum[0], sum[1]));
+      l += sums.x + sums.y;
       tmem_wait_st();
       dec::tc_fence_before();
-      mbar_arrive(&b.p_full[i]);
+      mbar_arrive(&b.p_full[i][j % kBufs]);
     }
     // ---- results
-    if (ok && n[i] > 0) {
-      ok = __all_sync(0xffffffffu, wait(&b.o_full[i], 0, &b.dead));
+    if (ok && n > 0) {
+      // with two buffers S(n - 1) tells that P V of step n - 3 is done, and a phase is told from the one two before it only
+      // after that one's end
+      if (kBufs == 2 && n > 1) ok = wait(&b.pv_done[i], (n - 2) & 1, &b.dead);
+      ok = __all_sync(0xffffffffu, ok && wait(&b.pv_done[i], (n - 1) & 1, &b.dead));
       dec::tc_fence_after();
     }
     const bool live = row < r.lq;
@@ -299,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
-      if (ok && n[i] > 0) {
-        dec::tmem_ld32(tO[i] + lanes + c * 32, o);
+      if (ok && n > 0) {
+        dec::tmem_ld32(tO(i) + lanes + c * 32, o);
         dec::tmem_wait_ld();
       } else {
 #pragma unroll
@@ -333,77 +422,93 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == 9) {
-      // ---- loads: Q once, then K0 V0 K1 V1 ... round the ring
-      if (lane == 0 && n_max > 0) {
-        const int tiles_q = n[1] > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(&b.q_full, tiles_q * Sh::kTile);
+      // ---- loads
+      if (n_max > 0 && elect()) {
+        const int tiles_q = n1 > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(&b.q_full, tiles_q * Sh::kQ);
         for (int i = 0; i < tiles_q; ++i)
           for (int c = 0; c < kSlabs; ++c)
-            tma_load(sm + i * Sh::kTile + c * kSlab, &q_map, c * 64, head, (int)r.q0 + m0 + i * kM, &b.q_full);
-        int slot = 0, issued = 0;
-        uint32_t round = 0;
-        for (int j = 0; j < 2 * n_max; ++j) {
-          if (round > 0 && !wait(&b.kv_empty[slot], (round - 1) & 1, &b.dead)) break;
+            tma_load(sm + i * Sh::kQ + c * kM * kRow, &q_map, c * 64, head0 + (pair ? i : 0), (int)r.q0 + m0 + i * mstep,
+                     &b.q_full);
+        int issued = 0;
+        auto load = [&](const CUtensorMap* map, int j) {
+          const int slot = issued % Sh::kStages, round = issued / Sh::kStages;
+          if (round > 0 && !wait(&b.kv_empty[slot], (round - 1) & 1, &b.dead)) return false;
           mbar_arrive_expect_tx(&b.kv_full[slot], Sh::kTile);
-          uint8_t* dst = sm + (2 + slot) * Sh::kTile;
           for (int c = 0; c < kSlabs; ++c)
-            tma_load(dst + c * kSlab, j & 1 ? &v_map : &k_map, c * 64, kvh, (int)r.k0 + (j >> 1) * kN, &b.kv_full[slot]);
+            tma_load(ring + slot * Sh::kTile + c * kN * kRow, map, c * 64, kvh, (int)r.k0 + j * kN, &b.kv_full[slot]);
           ++issued;
-          if (++slot == Sh::kStages) slot = 0, ++round;
+          return true;
+        };
+        bool ok = true;
+        for (int j = 0; j < kBufs && j < n_max; ++j) ok = ok && load(&k_map, j);
+        for (int j = 0; j < n_max && ok; ++j) {
+          ok = load(&v_map, j);
+          if (j + kBufs < n_max) ok = ok && load(&k_map, j + kBufs);
         }
         if (b.dead) {  // no copy may be in flight when the block ends
           wait_slow(&b.q_full, 0, nullptr);
-          for (int j = max(0, issued - Sh::kStages); j < issued; ++j)
-            wait_slow(&b.kv_full[j % Sh::kStages], (j / Sh::kStages) & 1, nullptr);
+          for (int x = max(0, issued - Sh::kStages); x < issued; ++x)
+            wait_slow(&b.kv_full[x % Sh::kStages], (x / Sh::kStages) & 1, nullptr);
         }
       }
     } else if (warp == 8) {
       // ---- MMAs
-      if (lane == 0 && n_max > 0) {
+      if (n_max > 0) {
         bool ok = wait(&b.q_full, 0, &b.dead);
-        auto full = [&](int j) {
-          ok = ok && wait(&b.kv_full[j % Sh::kStages], (j / Sh::kStages) & 1, &b.dead);
-          return smem_u32(sm + (2 + j % Sh::kStages) * Sh::kTile);
+        auto full = [&](int x) {
+          ok = ok && wait(&b.kv_full[x % Sh::kStages], (x / Sh::kStages) & 1, &b.dead);
+          return x % Sh::kStages * (Sh::kTile >> 4);
         };
-        auto scores = [&](int i, uint32_t kt) {
-          const uint32_t qt = smem_u32(sm + i * Sh::kTile);
-  #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t at = (ks / 4) * kSlab + (ks % 4) * 32;
-            dec::tc_mma(tS[i], desc(qt + at, 16), desc(kt + at, 16), kIdS, ks != 0);
+        auto release = [&](int x) {  // the last loads' slots are not filled again
+          if (x + Sh::kStages < 2 * n_max && elect()) dec::tc_commit(&b.kv_empty[x % Sh::kStages]);
+        };
+        const uint64_t q_desc = desc(smem_u32(sm), 16), k_desc = desc(smem_u32(ring), 16),
+                       v_desc = desc(smem_u32(ring), kN * kRow);
+        auto scores = [&](int i, int j, uint32_t kt) {
+          if (elect()) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              dec::tc_mma(tS(i, j), q_desc + ((i * Sh::kQ + (ks / 4) * kM * kRow + (ks % 4) * 32) >> 4),
+                          k_desc + kt + (((ks / 4) * kN * kRow + (ks % 4) * 32) >> 4), kIdS, ks != 0);
+            dec::tc_commit(&b.s_full[i][j % kBufs]);
           }
-          dec::tc_commit(&b.s_full[i]);
+          __syncwarp();
         };
         auto values = [&](int i, int j, uint32_t vt) {
-  #pragma unroll
-          for (int ks = 0; ks < kN / 16; ++ks)
-            mma_ts(tO[i], tS[i] + ks * 8, desc(vt + ks * 16 * 128, kSlab), kIdO, j != 0 || ks != 0);
-          if (j == n[i] - 1) dec::tc_commit(&b.o_full[i]);
+          if (elect()) {
+#pragma unroll
+            for (int ks = 0; ks < kN / 16; ++ks)
+              mma_ts(tO(i), tS(i, j) + ks * 8, v_desc + vt + ((ks * 16 * kRow) >> 4), kIdO, ks != 0 ? 1 : j != 0);
+            dec::tc_commit(&b.pv_done[i]);
+          }
+          __syncwarp();
         };
-        uint32_t kt = full(0);
-        dec::tc_fence_after();
-        for (int i = 0; i < 2; ++i)
-          if (ok && n[i] > 0) scores(i, kt);
-        auto release = [&](int j) {  // the last loads' slots are not filled again
-          if (ok && j + Sh::kStages < 2 * n_max) dec::tc_commit(&b.kv_empty[j % Sh::kStages]);
-        };
-        release(0);
-        for (int j = 0; j < n_max && ok; ++j) {
-          const uint32_t vt = full(2 * j + 1);
-          if (j + 1 < n_max) kt = full(2 * j + 2);
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (j >= n[i]) continue;
-            ok = wait(&b.p_full[i], j & 1, &b.dead);
-            if (!ok) break;
+        for (int j = 0; j < kBufs && j < n_max; ++j) {
+          const uint32_t kt = full(k_at(j));
+          if (!__all_sync(0xffffffffu, ok)) break;
+          dec::tc_fence_after();
+          if (j < n0) scores(0, j, kt);
+          if (j < n1) scores(1, j, kt);
+          release(k_at(j));
+        }
+        for (int j = 0; j < n_max && __all_sync(0xffffffffu, ok); ++j) {
+          const uint32_t vt = full(v_at(j)), kt = j + kBufs < n_max ? full(k_at(j + kBufs)) : 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int n = i ? n1 : n0;
+            if (j >= n) continue;
+            ok = ok && wait(&b.p_full[i][j % kBufs], (j / kBufs) & 1, &b.dead);
+            if (!__all_sync(0xffffffffu, ok)) break;
             dec::tc_fence_after();
             values(i, j, vt);
-            if (j + 1 < n[i]) scores(i, kt);
+            if (j + kBufs < n) scores(i, j + kBufs, kt);
           }
-          release(2 * j + 1);
-          release(2 * j + 2);
+          release(v_at(j));
+          if (j + kBufs < n_max) release(k_at(j + kBufs));
         }
-        if (!ok) {  // nor any MMA
-          dec::tc_commit(&b.drained);
+        if (!__all_sync(0xffffffffu, ok)) {  // nor any MMA
+          if (elect()) dec::tc_commit(&b.drained);
           wait_slow(&b.drained, 0, nullptr);
         }
       }
@@ -417,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The bytes of a tensor of rows [rows][heads][D] as 128-row, 64-element boxes.
-inline bool make_map(CUtensorMap* m, const void* base, int rows, int heads, int d, int64_t stride) {
+// A tensor of rows [rows][heads][D] in boxes of `tile` rows and 64 elements.
+inline bool make_map(CUtensorMap* m, const void* base, int rows, int heads, int d, int64_t stride, int tile) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -434,7 +539,7 @@ inline bool make_map(CUtensorMap* m, const void* base, int rows, int heads, int 
   if (!encode) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t box[3] = {64, 1, 128}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)tile}, step[3] = {1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -445,9 +550,10 @@ cudaError_t launch(const PrefillArgs& a, int n_seqs, cudaStream_t st) {
   using Sh = Shape<D>;
   CUtensorMap q, k, v;
   const bool keys = a.n_k > 0;  // without keys every row is zero and no load is issued
-  if (!make_map(&q, a.q, a.n_q, a.heads, D, a.qs) ||
-      !make_map(&k, keys ? a.k : a.q, keys ? a.n_k : a.n_q, keys ? a.heads / a.gs : a.heads, D, keys ? a.ks : a.qs) ||
-      !make_map(&v, keys ? a.v : a.q, keys ? a.n_k : a.n_q, keys ? a.heads / a.gs : a.heads, D, keys ? a.vs : a.qs))
+  const void *kp = keys ? a.k : a.q, *vp = keys ? a.v : a.q;
+  const int rows = keys ? a.n_k : a.n_q, heads = keys ? a.heads / a.gs : a.heads;
+  if (!make_map(&q, a.q, a.n_q, a.heads, D, a.qs, kM) || !make_map(&k, kp, rows, heads, D, keys ? a.ks : a.qs, Sh::kN) ||
+      !make_map(&v, vp, rows, heads, D, keys ? a.vs : a.qs, Sh::kN))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
   if (e != cudaSuccess) return e;
@@ -456,8 +562,9 @@ cudaError_t launch(const PrefillArgs& a, int n_seqs, cudaStream_t st) {
     return cudaFuncGetAttributes(&f, prefill_kernel<D>) == cudaSuccess ? f.numRegs : 0;
   }();
   if (regs != kRegs) return cudaErrorInvalidValue;  // the warps would wait for registers that are not there
-  const int tiles = (a.max_q + 2 * kM - 1) / (2 * kM);
-  prefill_kernel<D><<<(unsigned)((int64_t)n_seqs * tiles * a.heads), kThreads, Sh::kSmem, st>>>(q, k, v, a, n_seqs);
+  const int pair = a.gs % 2 == 0, rows_q = pair ? kM : 2 * kM;
+  const int64_t blocks = (int64_t)n_seqs * ((a.max_q + rows_q - 1) / rows_q) * (pair ? a.heads / 2 : a.heads);
+  prefill_kernel<D><<<(unsigned)blocks, kThreads, Sh::kSmem, st>>>(q, k, v, a, n_seqs, pair);
   return cudaGetLastError();
 }
 
