@@ -1,16 +1,16 @@
 // Attention of packed bf16 prompts on tcgen05 tensor cores.
 //
 // A block takes two tiles of 128 queries that read the same keys (two heads of one kv head, or neighbouring queries
-// of one head), and walks their keys 64 at a time:
-//   S = Q K^T (128 x 64, fp32 in TMEM), P = 2^(scale log2(e) S - m) rounded to bf16 over S, O += P V.
-// Warps 0-3 and 4-7 are the tiles' softmax, a thread a row; warp 8 issues every MMA; warp 9 every TMA load.
-//   TMEM: S of tile 0, two buffers of 64 columns (P in the first 32 of each) | S of tile 1 | O0 | O1 (D columns each)
+// of one head), and walks their keys 128 at a time:
+//   S = Q K^T (128 x 128, fp32 in TMEM), P = 2^(scale log2(e) S - m) rounded to bf16 over S, O += P V.
+// Warps 0-3 and 4-7 are the tiles' softmax, a thread a row; warp 8 issues every MMA; warp 9 every TMA load.  The softmax
+// keeps a row of S in registers: it takes them over from the last warpgroup (208 and 88 of the 168 at launch).
+//   TMEM: S0 | S1 (128 columns each, P in the first 64) | O0 | O1 (D columns each)
 //   shared memory: Q, and a ring of K and V tiles, rows of 128 bytes in the 128-byte swizzle
-// Each tile has the scores of two steps in TMEM, so its softmax goes from one step to the next while the tensor cores
-// do P V of the step before and Q K^T of the one after: neither waits for the other's latency.
-// One thread's MMAs complete in the order they were issued, so S_i(j + 2), issued behind P V_i(j), may overwrite P_i(j).
-// A row of O is rescaled only when the row's maximum has grown by more than 2^8 (P up to 2^8 and its sum lose
-// nothing); the softmax thread then waits for P V of the step before and does it in TMEM.
+// The tiles alternate: while one tile's softmax runs, the tensor cores do the other's P V and next Q K^T.
+// One thread's MMAs complete in the order they were issued.  So S_i(j + 1), issued behind P V_i(j), may overwrite P_i(j),
+// and once it has arrived O_i is at rest until the tile's next P: a softmax thread may rescale its row of O there.  It
+// does only when the row's maximum has grown by more than 2^8 (P up to 2^8 and its sum lose nothing).
 //
 // P is rounded to bf16 (2^-9 of each weight, of the same size as V's own rounding and the result's); its sum is
 // of the unrounded weights, in fp32.
@@ -63,34 +63,30 @@ using dec::smem_u32;
 
 constexpr int kThreads = 384, kRegs = 168, kRegsSoftmax = 208, kRegsRest = 88;
 static_assert(256 * kRegsSoftmax + 128 * kRegsRest <= kThreads * kRegs, "registers handed over are those at launch");
-constexpr int kM = 128;
+constexpr int kM = 128, kN = 128;
 #ifndef KPOLY
-#define KPOLY 2
+#define KPOLY 3
 #endif
 constexpr int kPoly = KPOLY;  // of every 8 pairs of a row, those whose exponentials are the polynomial's
 constexpr float kC0 = 0x1.fff692p-1f, kC1 = 0x1.62f31ap-1f, kC2 = 0x1.f0de1ap-3f, kC3 = 0x1.c3f75ep-5f;
 
 template <int D>
 struct Shape {
-#ifndef KN128
-#define KN128 128
-#define KN64 128
-#endif
-  static constexpr int kN = D == 128 ? KN128 : KN64;      // keys of a step
-  static constexpr int kBufs = kN == 128 ? 1 : 2;   // steps whose scores a tile has in TMEM
-  static constexpr int kStages = (D == 128 ? 128 : 96) * 1024 / (kN * D * 2);
-  static constexpr int kQ = kM * D * 2, kTile = kN * D * 2;  // bytes of a query tile, of a step's keys or values
-  static constexpr int kSmem = 2 * kQ + kStages * kTile + 512;  // barriers behind the tiles;  // over half an SM's: one block, and its 512 TMEM columns, per SM
+  static constexpr int kTile = 128 * D * 2;  // bytes of 128 queries, keys or values
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kSmem = (2 + kStages) * kTile + 512;  // barriers behind the tiles; over half an SM's, so a block has
+                                                             // its SM, and all of its 512 TMEM columns, to itself
 };
 
 struct Bars {
-  uint64_t q_full, kv_full[12], kv_empty[12], s_full[2][2], p_full[2][2], pv_done[2], drained;
+  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], drained;
   uint32_t tmem;
   int dead;
 };
 
-// One lane of a converged warp.  (Under `lane == 0` the compiler takes the branch for divergent and moves every operand
-// of an MMA to the uniform registers by itself: issuing then took longer than the MMAs.)
+// One lane of a converged warp.  What an MMA is issued with must be the same for the warp in the compiler's eyes too: the
+// issuing warp's loops run in all lanes, over values from shuffles and votes.  Under `lane == 0`, or with loop bounds
+// straight from memory, an MMA took about 145 cycles to issue; so it takes its 64.
 __device__ __forceinline__ bool elect() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -115,6 +111,12 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead) 
   for (int i = 0; i < 16; ++i)
     if (dec::mbar_try_wait(bar, parity)) return true;
   return wait_slow(bar, parity, dead);
+}
+// The same for a whole warp, whose lanes stay together.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* dead) {
+  for (int i = 0; i < 16; ++i)
+    if (__all_sync(0xffffffffu, dec::mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_slow(bar, parity, dead));
 }
 
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int head, int row, uint64_t* bar) {
@@ -239,11 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap v_map, const PrefillArgs a, const int n_seqs, const int pair) {
   using Sh = Shape<D>;
   using bf16 = __nv_bfloat16;
-  constexpr int kN = Sh::kN, kBufs = Sh::kBufs, kSlabs = D / 64, kRow = 128;  // slabs of 64 elements: rows of 128 bytes
+  constexpr int kSlabs = D / 64, kRow = 128, kSlab = 128 * kRow;  // slabs of 64 elements: rows of 128 bytes
   constexpr uint32_t kIdS = dec::umma_idesc_bf16(kM, kN, false), kIdO = dec::umma_idesc_bf16(kM, D, true);
   extern __shared__ __align__(1024) uint8_t sm[];
-  Bars& b = *reinterpret_cast<Bars*>(sm + 2 * Sh::kQ + Sh::kStages * Sh::kTile);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Bars& b = *reinterpret_cast<Bars*>(sm + 2 * Sh::kTile + Sh::kStages * Sh::kTile);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   // pair: the tiles are heads 2x and 2x + 1; else queries m0 and m0 + 128
   const int columns = pair ? a.heads / 2 : a.heads;
   const int head0 = (pair ? 2 : 1) * (blockIdx.x % columns), s = blockIdx.x / columns % n_seqs;
@@ -258,15 +260,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int keys = !r.ok || mi >= r.lq ? 0 : a.causal ? min(r.lk, min(mi + kM, r.lq) + shift) : r.lk;
     return keys > 0 ? (keys + kN - 1) / kN : 0;
   };
-  const int n0 = steps(0), n1 = steps(1), n_max = max(n0, n1);
+  const int n0 = __shfl_sync(0xffffffffu, steps(0), 0), n1 = __shfl_sync(0xffffffffu, steps(1), 0), n_max = max(n0, n1);
 
-  uint8_t* ring = sm + 2 * Sh::kQ;
+  uint8_t* ring = sm + 2 * Sh::kTile;
   if (tid == 0) {
     dec::mbar_init(&b.q_full, 1);
     for (int i = 0; i < Sh::kStages; ++i) dec::mbar_init(&b.kv_full[i], 1), dec::mbar_init(&b.kv_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      for (int k = 0; k < 2; ++k) dec::mbar_init(&b.s_full[i][k], 1), dec::mbar_init(&b.p_full[i][k], kM);
-      dec::mbar_init(&b.pv_done[i], 1);
+      dec::mbar_init(&b.s_full[i], 1);
+      dec::mbar_init(&b.p_full[i], kM);
+      dec::mbar_init(&b.o_full[i], 1);
     }
     dec::mbar_init(&b.drained, 1);
     b.dead = 0;
@@ -279,12 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   dec::tc_fence_before();
   __syncthreads();
   dec::tc_fence_after();
-  constexpr uint32_t tm = 0;  // all 512 columns are this block's
-  auto tS = [&](int i, int j) { return tm + (i * kBufs + j % kBufs) * kN; };
-  auto tO = [&](int i) { return tm + 256 + i * D; };
-  // place in the order of loads: kBufs of K, then V0 and the next K, V1 and the next ...
-  auto k_at = [&](int j) { return j < kBufs ? j : 2 * j - kBufs + 1; };
-  auto v_at = [&](int j) { return min(2 * j + kBufs, n_max + j); };
+  // All 512 columns are this block's, so they begin at 0.
+  auto tS = [](int i) { return (uint32_t)(i * kN); };
+  auto tO = [](int i) { return (uint32_t)(2 * kN + i * D); };
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -297,12 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      ok = __all_sync(0xffffffffu, wait(&b.s_full[i][j % kBufs], (j / kBufs) & 1, &b.dead));
+      ok = __all_sync(0xffffffffu, wait(&b.s_full[i], j & 1, &b.dead));
       if (!ok) break;
       dec::tc_fence_after();
       uint32_t x[kN / 32][32];
 #pragma unroll
-      for (int c = 0; c < kN / 32; ++c) dec::tmem_ld32(tS(i, j) + lanes + c * 32, x[c]);
+      for (int c = 0; c < kN / 32; ++c) dec::tmem_ld32(tS(i) + lanes + c * 32, x[c]);
       dec::tmem_wait_ld();
       const bool masked = j * kN + kN > warp_end;
       if (masked) {
@@ -323,10 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= f;
         m = mn;
         if (j > 0) {
-          // (S(j) was issued behind P V of step j - 2, so this phase is the one after that)
-          ok = __all_sync(0xffffffffu, wait(&b.pv_done[i], (j - 1) & 1, &b.dead));
-          if (!ok) break;
-          dec::tc_fence_after();
+          // S(j) was issued behind P V of the step before: O is at rest until this step's P
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -360,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const __nv_bfloat162 h = __floats2bfloat162_rn(u.x, u.y);
             p[e] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          tmem_st32(tS(i, j) + lanes + c * 32, p);
+          tmem_st32(tS(i) + lanes + c * 32, p);
         }
       };
       if (masked)  // an unseen key's weight is exactly zero
@@ -371,14 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       l += sums.x + sums.y;
       tmem_wait_st();
       dec::tc_fence_before();
-      mbar_arrive(&b.p_full[i][j % kBufs]);
+      mbar_arrive(&b.p_full[i]);
     }
     // ---- results
     if (ok && n > 0) {
-      // with two buffers S(n - 1) tells that P V of step n - 3 is done, and a phase is told from the one two before it only
-      // after that one's end
-      if (kBufs == 2 && n > 1) ok = wait(&b.pv_done[i], (n - 2) & 1, &b.dead);
-      ok = __all_sync(0xffffffffu, ok && wait(&b.pv_done[i], (n - 1) & 1, &b.dead));
+      ok = __all_sync(0xffffffffu, wait(&b.o_full[i], 0, &b.dead));
       dec::tc_fence_after();
     }
     const bool live = row < r.lq;
@@ -425,10 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- loads
       if (n_max > 0 && elect()) {
         const int tiles_q = n1 > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(&b.q_full, tiles_q * Sh::kQ);
+        mbar_arrive_expect_tx(&b.q_full, tiles_q * Sh::kTile);
         for (int i = 0; i < tiles_q; ++i)
           for (int c = 0; c < kSlabs; ++c)
-            tma_load(sm + i * Sh::kQ + c * kM * kRow, &q_map, c * 64, head0 + (pair ? i : 0), (int)r.q0 + m0 + i * mstep,
+            tma_load(sm + i * Sh::kTile + c * kSlab, &q_map, c * 64, head0 + (pair ? i : 0), (int)r.q0 + m0 + i * mstep,
                      &b.q_full);
         int issued = 0;
         auto load = [&](const CUtensorMap* map, int j) {
@@ -436,16 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (round > 0 && !wait(&b.kv_empty[slot], (round - 1) & 1, &b.dead)) return false;
           mbar_arrive_expect_tx(&b.kv_full[slot], Sh::kTile);
           for (int c = 0; c < kSlabs; ++c)
-            tma_load(ring + slot * Sh::kTile + c * kN * kRow, map, c * 64, kvh, (int)r.k0 + j * kN, &b.kv_full[slot]);
+            tma_load(ring + slot * Sh::kTile + c * kSlab, map, c * 64, kvh, (int)r.k0 + j * kN, &b.kv_full[slot]);
           ++issued;
           return true;
         };
         bool ok = true;
-        for (int j = 0; j < kBufs && j < n_max; ++j) ok = ok && load(&k_map, j);
-        for (int j = 0; j < n_max && ok; ++j) {
-          ok = load(&v_map, j);
-          if (j + kBufs < n_max) ok = ok && load(&k_map, j + kBufs);
-        }
+        for (int j = 0; j < n_max && ok; ++j) ok = load(&k_map, j) && load(&v_map, j);
         if (b.dead) {  // no copy may be in flight when the block ends
           wait_slow(&b.q_full, 0, nullptr);
           for (int x = max(0, issued - Sh::kStages); x < issued; ++x)
@@ -455,59 +445,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 8) {
       // ---- MMAs
       if (n_max > 0) {
-        bool ok = wait(&b.q_full, 0, &b.dead);
+        bool ok = wait_warp(&b.q_full, 0, &b.dead);
         auto full = [&](int x) {
-          ok = ok && wait(&b.kv_full[x % Sh::kStages], (x / Sh::kStages) & 1, &b.dead);
+          ok = ok && wait_warp(&b.kv_full[x % Sh::kStages], (x / Sh::kStages) & 1, &b.dead);
           return x % Sh::kStages * (Sh::kTile >> 4);
         };
         auto release = [&](int x) {  // the last loads' slots are not filled again
           if (x + Sh::kStages < 2 * n_max && elect()) dec::tc_commit(&b.kv_empty[x % Sh::kStages]);
         };
         const uint64_t q_desc = desc(smem_u32(sm), 16), k_desc = desc(smem_u32(ring), 16),
-                       v_desc = desc(smem_u32(ring), kN * kRow);
-        auto scores = [&](int i, int j, uint32_t kt) {
+                       v_desc = desc(smem_u32(ring), kSlab);
+        auto scores = [&](int i, uint32_t kt) {
           if (elect()) {
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-              dec::tc_mma(tS(i, j), q_desc + ((i * Sh::kQ + (ks / 4) * kM * kRow + (ks % 4) * 32) >> 4),
-                          k_desc + kt + (((ks / 4) * kN * kRow + (ks % 4) * 32) >> 4), kIdS, ks != 0);
-            dec::tc_commit(&b.s_full[i][j % kBufs]);
+              dec::tc_mma(tS(i), q_desc + ((i * Sh::kTile + (ks / 4) * kSlab + (ks % 4) * 32) >> 4),
+                          k_desc + kt + (((ks / 4) * kSlab + (ks % 4) * 32) >> 4), kIdS, ks != 0);
+            dec::tc_commit(&b.s_full[i]);
           }
           __syncwarp();
         };
-        auto values = [&](int i, int j, uint32_t vt) {
+        auto values = [&](int i, int j, int n, uint32_t vt) {
           if (elect()) {
 #pragma unroll
             for (int ks = 0; ks < kN / 16; ++ks)
-              mma_ts(tO(i), tS(i, j) + ks * 8, v_desc + vt + ((ks * 16 * kRow) >> 4), kIdO, ks != 0 ? 1 : j != 0);
-            dec::tc_commit(&b.pv_done[i]);
+              mma_ts(tO(i), tS(i) + ks * 8, v_desc + vt + ((ks * 16 * kRow) >> 4), kIdO, ks != 0 ? 1 : j != 0);
+            if (j + 1 == n) dec::tc_commit(&b.o_full[i]);
           }
           __syncwarp();
         };
-        for (int j = 0; j < kBufs && j < n_max; ++j) {
-          const uint32_t kt = full(k_at(j));
-          if (!__all_sync(0xffffffffu, ok)) break;
+        uint32_t kt = full(0);
+        if (ok) {
           dec::tc_fence_after();
-          if (j < n0) scores(0, j, kt);
-          if (j < n1) scores(1, j, kt);
-          release(k_at(j));
+          if (n0 > 0) scores(0, kt);
+          if (n1 > 0) scores(1, kt);
+          release(0);
         }
-        for (int j = 0; j < n_max && __all_sync(0xffffffffu, ok); ++j) {
-          const uint32_t vt = full(v_at(j)), kt = j + kBufs < n_max ? full(k_at(j + kBufs)) : 0;
+        for (int j = 0; j < n_max && ok; ++j) {
+          const uint32_t vt = full(2 * j + 1);
+          if (j + 1 < n_max) kt = full(2 * j + 2);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int n = i ? n1 : n0;
             if (j >= n) continue;
-            ok = ok && wait(&b.p_full[i][j % kBufs], (j / kBufs) & 1, &b.dead);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            ok = ok && wait_warp(&b.p_full[i], j & 1, &b.dead);
+            if (!ok) break;
             dec::tc_fence_after();
-            values(i, j, vt);
-            if (j + kBufs < n) scores(i, j + kBufs, kt);
+            values(i, j, n, vt);
+            if (j + 1 < n) scores(i, kt);
           }
-          release(v_at(j));
-          if (j + kBufs < n_max) release(k_at(j + kBufs));
+          release(2 * j + 1);
+          release(2 * j + 2);
         }
-        if (!__all_sync(0xffffffffu, ok)) {  // nor any MMA
+        if (!ok) {  // nor any MMA
           if (elect()) dec::tc_commit(&b.drained);
           wait_slow(&b.drained, 0, nullptr);
         }
@@ -518,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     __syncwarp();
     dec::tc_fence_after();
-    dec::tmem_dealloc(tm, 512);
+    dec::tmem_dealloc(0, 512);
   }
 }
 
@@ -552,8 +542,8 @@ cudaError_t launch(const PrefillArgs& a, int n_seqs, cudaStream_t st) {
   const bool keys = a.n_k > 0;  // without keys every row is zero and no load is issued
   const void *kp = keys ? a.k : a.q, *vp = keys ? a.v : a.q;
   const int rows = keys ? a.n_k : a.n_q, heads = keys ? a.heads / a.gs : a.heads;
-  if (!make_map(&q, a.q, a.n_q, a.heads, D, a.qs, kM) || !make_map(&k, kp, rows, heads, D, keys ? a.ks : a.qs, Sh::kN) ||
-      !make_map(&v, vp, rows, heads, D, keys ? a.vs : a.qs, Sh::kN))
+  if (!make_map(&q, a.q, a.n_q, a.heads, D, a.qs, kM) || !make_map(&k, kp, rows, heads, D, keys ? a.ks : a.qs, kN) ||
+      !make_map(&v, vp, rows, heads, D, keys ? a.vs : a.qs, kN))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
   if (e != cudaSuccess) return e;
