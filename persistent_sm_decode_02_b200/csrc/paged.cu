@@ -15,6 +15,8 @@ struct Cache {
 };
 
 // ------------------------------------------------------------------ append
+enum { kKeysValues = 1, kQueries = 2, kBoth = 3 };  // what a launch does
+
 struct AppendArgs {
   Cache c;
   const double* inv_freq;
@@ -23,7 +25,8 @@ struct AppendArgs {
   const void *q, *k, *v;
   void* q_out;
   int64_t qs, ks, vs, qos;
-  int gs, n_tokens, max_new, pieces, hpc;  // gs: query heads per kv head (0: no q); hpc: kv heads per block
+  int heads, n_tokens, max_new, pieces;  // heads: of q (0: no q)
+  int kv_blocks, q_blocks;               // of one (sequence, page): they share its kv heads, and its query heads, evenly
   const int32_t *cu, *lens, *table;
   int table_stride;
   int32_t* status;
@@ -55,15 +58,36 @@ __device__ __forceinline__ float amax_finite(float m, float x) {
   return a <= FLT_MAX ? fmaxf(m, a) : m;
 }
 
+// sin and cos of an angle in turns, to about half an ulp of fp32.  Quarter turns are taken off in fp64 (a far
+// position makes many); on the +-pi/4 left, as a pair of floats, the Taylor series with the leading terms kept exact.
+__device__ __forceinline__ void sincos_turns(double turns, float& sn, float& cs) {
+  const double q = turns * 4.0, k = rint(q), x = (q - k) * 1.5707963267948966;
+  const float h = (float)x, l = (float)(x - (double)h), z = h * h;
+  const float ps = fmaf(fmaf(fmaf(1.f / 362880.f, z, -1.f / 5040.f), z, 1.f / 120.f), z, -1.f / 6.f);
+  const float s = h + fmaf(h * z, ps, l);
+  const float pc = fmaf(fmaf(fmaf(-1.f / 3628800.f, z, 1.f / 40320.f), z, -1.f / 720.f), z, 1.f / 24.f);
+  const float w = fmaf(-0.5f, z, 1.f);
+  // 1 - z / 2 is w + (1 - w - z / 2), and h * h is z + fma(h, h, -z)
+  const float c = w + fmaf(z * z, pc, fmaf(-0.5f, z, 1.f - w) - fmaf(0.5f, fmaf(h, h, -z), h * l));
+  const int quarter = (int)(long long)k & 3;
+  sn = quarter & 1 ? c : s;
+  cs = quarter & 1 ? s : c;
+  if (quarter & 2) sn = -sn;
+  if ((quarter + 1) & 2) cs = -cs;
+}
+
 // Sixteen values of one row, in the two 8-element chunks a thread holds, turned by their eight angles.
 __device__ __forceinline__ void rotate16(float* x, const float* cs, const float* sn, bool neighbour) {
+  if (neighbour) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (neighbour) {
+    for (int i = 0; i < 8; ++i) {
       const float a = x[2 * i], b = x[2 * i + 1];
       x[2 * i] = a * cs[i] - b * sn[i];
       x[2 * i + 1] = a * sn[i] + b * cs[i];
-    } else {
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
       const float a = x[i], b = x[8 + i];
       x[i] = a * cs[i] - b * sn[i];
       x[8 + i] = a * sn[i] + b * cs[i];
@@ -78,9 +102,22 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float* x, float in
   *reinterpret_cast<uint2*>(p) = o;
 }
 
+// The block's maxima, in every thread.
+__device__ __forceinline__ void block_max(float (*red)[16], float& x, float& y) {
+  x = warp_max(x);
+  y = warp_max(y);
+  if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = x, red[1][threadIdx.x >> 5] = y;
+  __syncthreads();
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+    x = fmaxf(x, red[0][w]);
+    y = fmaxf(y, red[1][w]);
+  }
+}
+
 // Rows before the piece, rounded again for a larger scale.
-__device__ __forceinline__ void rescale_rows(uint8_t* p, int bytes, float ratio) {
-  for (int i = threadIdx.x * 8; i < bytes; i += blockDim.x * 8) {
+__device__ __forceinline__ void rescale_rows(uint8_t* p, int bytes, float ratio, int thread, int threads) {
+#pragma unroll 4
+  for (int i = thread * 8; i < bytes; i += threads * 8) {
     uint2 w = *reinterpret_cast<const uint2*>(p + i);
     const float2 a = from_e4m3x2(w.x), b = from_e4m3x2(w.x >> 16), c = from_e4m3x2(w.y), d = from_e4m3x2(w.y >> 16);
     const float x[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
@@ -88,139 +125,214 @@ __device__ __forceinline__ void rescale_rows(uint8_t* p, int bytes, float ratio)
   }
 }
 
-// One block per (sequence, page it touches, hpc kv heads).  A thread holds the same 16 dims of its rows for
-// every head, so it computes their 8 angles once (fp64 turns, reduced to +-1/2, then fp32 sin and cos).
-template <typename T, int D, int NIT>
-__global__ void __launch_bounds__(512) append_kernel(AppendArgs a) {
+// New tokens of sequence s in one page.
+struct Piece {
+  int64_t lo, row0;  // first position, its row of q, k and v
+  int rows, slot, page;
+};
+__device__ __forceinline__ bool piece_of(const AppendArgs& a, int s, int piece, Piece& p) {
+  const int ps = a.c.ps;
+  const int64_t c0 = a.cu[s], c1 = a.cu[s + 1], n = c1 - c0, len = a.lens[s];
+  if (n == 0) return false;
+  if (n < 0 || c0 < 0 || c1 > a.n_tokens || n > a.max_new || len < n || len > (int64_t)a.table_stride * ps) {
+    if (threadIdx.x == 0) flag(a.status, DEC_SEQ_BAD_RANGE);
+    return false;
+  }
+  const int64_t start = len - n, pi = start / ps + piece, hi = min(len, (pi + 1) * ps);
+  p.lo = max(start, pi * ps);
+  if (p.lo >= hi) return false;
+  p.row0 = c0 + (p.lo - start);
+  p.rows = (int)(hi - p.lo);
+  p.slot = (int)(p.lo - pi * ps);
+  p.page = a.table[(int64_t)s * a.table_stride + pi];
+  return true;
+}
+
+// The eight angles of a thread's dims at position pos.
+__device__ __forceinline__ void angles(const AppendArgs& a, int c, int64_t pos, float* sn, float* cs) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    sincos_turns((double)pos * a.inv_freq[8 * c + i] * 0.15915494309189535, sn[i], cs[i]);  // 1 / (2 pi)
+    sn[i] *= a.factor;
+    cs[i] *= a.factor;
+  }
+}
+
+// Blocks of a (sequence, page it touches): some for its kv heads, some for its query heads.  A thread holds the same 16
+// dims of its rows for every head, so it computes their 8 angles once.  Bound by memory where tokens are many (4 x 8192
+// tokens, 32 / 8 heads of 128, bf16: 738 MB in 138 us, 5.3 TB/s), by the chain of dependent loads (offsets, page id,
+// row) where they are few (one token 3.8 us).  A page's scale needs all of its new values, so its keys and values stay in
+// registers between the maximum and the rounding and are read once; the next head's are on their way meanwhile.
+template <typename T, int D, int NIT, int ROLE>
+__global__ void __launch_bounds__(ROLE == kQueries ? 256 : 512, ROLE == kQueries ? 3 : ROLE == kKeysValues && NIT == 1 ? 2 : 1)
+    append_kernel(AppendArgs a) {
   __shared__ float red[2][2][16];
   constexpr int kUnits = D / 16;  // threads a row
-  const int groups = a.c.hkv / a.hpc;
-  const int hg = blockIdx.x % groups, piece = blockIdx.x / groups % a.pieces, s = blockIdx.x / groups / a.pieces;
+  constexpr int kBatch = 4;       // query heads whose loads are under way at once
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int blocks = (ROLE & kKeysValues ? a.kv_blocks : 0) + (ROLE & kQueries ? a.q_blocks : 0);
+  const int part = blockIdx.x % blocks, piece = blockIdx.x / blocks % a.pieces, s = blockIdx.x / blocks / a.pieces;
   const int tid = threadIdx.x, ps = a.c.ps;
-  const int64_t c0 = a.cu[s], c1 = a.cu[s + 1], n = c1 - c0;
-  const int64_t len = a.lens[s];
-  if (n == 0) return;
-  if (n < 0 || c0 < 0 || c1 > a.n_tokens || n > a.max_new || len < n || len > (int64_t)a.table_stride * ps) {
-    if (tid == 0) flag(a.status, DEC_SEQ_BAD_RANGE);
-    return;
-  }
-  const int64_t start = len - n, pi = start / ps + piece;
-  const int64_t lo = max(start, pi * ps), hi = min(len, (pi + 1) * ps);
-  if (lo >= hi) return;
-  const int page = a.table[(int64_t)s * a.table_stride + pi];
-  const bool page_ok = page >= 0 && page < a.c.n_pages;
-  if (!page_ok && tid == 0) flag(a.status, DEC_SEQ_BAD_PAGE);
-  const int nr = (int)(hi - lo), slot0 = (int)(lo - pi * ps);
-  const int64_t row0 = c0 + (lo - start);
+  Piece p;
+  if (!piece_of(a, s, piece, p)) return;
+  const int nr = p.rows, slot0 = p.slot, page = p.page;
+  const int64_t row0 = p.row0;
   const bool neighbour = a.neighbour;
 
   const int c = tid % kUnits;  // blockDim.x is a multiple of kUnits
   const bool turned = c < a.rot / 16;
   const int d0 = turned && !neighbour ? 8 * c : 16 * c, d1 = turned && !neighbour ? a.rot / 2 + 8 * c : 16 * c + 8;
+  const int q_part = part - (ROLE & kKeysValues ? a.kv_blocks : 0);
+  if ((ROLE & kQueries) && q_part >= 0) {  // ---- query heads
+    const int h0 = a.heads * q_part / a.q_blocks, h1 = a.heads * (q_part + 1) / a.q_blocks;
+    for (int r = tid / kUnits; r < nr; r += blockDim.x / kUnits) {
+      float cs[8], sn[8];
+      if (turned) angles(a, c, p.lo + r, sn, cs);
+      const T* qp = static_cast<const T*>(a.q) + (row0 + r) * a.qs;
+      T* op = static_cast<T*>(a.q_out) + (row0 + r) * a.qos;
+      for (int h = h0; h < h1; h += kBatch) {
+        Vec8<T> x[kBatch][2];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          if (h + b < h1) {
+            x[b][0].load(qp + (h + b) * D + d0);
+            x[b][1].load(qp + (h + b) * D + d1);
+          }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          if (h + b < h1) {
+            float y[16];
+            x[b][0].get(y);
+            x[b][1].get(y + 8);
+            if (turned) rotate16(y, cs, sn, neighbour);
+            Vec8<T>::store(op + (h + b) * D + d0, y);
+            Vec8<T>::store(op + (h + b) * D + d1, y + 8);
+          }
+      }
+    }
+    return;
+  }
+  if (!(ROLE & kKeysValues)) return;
+
+  // ---- keys and values
+  const bool page_ok = page >= 0 && page < a.c.n_pages;
+  if (!page_ok) {
+    if (tid == 0) flag(a.status, DEC_SEQ_BAD_PAGE);
+    return;
+  }
+  const int g0 = a.c.hkv * part / a.kv_blocks, g1 = a.c.hkv * (part + 1) / a.kv_blocks;
   float cs[NIT][8], sn[NIT][8];
   int row[NIT];
 #pragma unroll
   for (int it = 0; it < NIT; ++it) {
     row[it] = (tid + it * blockDim.x) / kUnits;
-    if (turned && row[it] < nr) {
-      const double pos = (double)(lo + row[it]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const double turns = pos * a.inv_freq[8 * c + i] * 0.15915494309189535;  // 1 / (2 pi)
-        float co, si;
-        sincospif(2.f * (float)(turns - rint(turns)), &si, &co);
-        cs[it][i] = co * a.factor;
-        sn[it][i] = si * a.factor;
-      }
-    }
+    if (turned && row[it] < nr) angles(a, c, p.lo + row[it], sn[it], cs[it]);
   }
-
-  for (int g = 0; g < a.hpc; ++g) {
-    const int head = hg * a.hpc + g;
-    float k[NIT][16], mk = 0.f, mv = 0.f;
-    Vec8<T> v[NIT][2];
+  Vec8<T> kr[NIT][2], vr[NIT][2];
+  auto load = [&](int head) {
 #pragma unroll
     for (int it = 0; it < NIT; ++it)
       if (row[it] < nr) {
         const T* kp = static_cast<const T*>(a.k) + (row0 + row[it]) * a.ks + (int64_t)head * D;
         const T* vp = static_cast<const T*>(a.v) + (row0 + row[it]) * a.vs + (int64_t)head * D;
-        Vec8<T> x[2];
-        x[0].load(kp + d0);
-        x[1].load(kp + d1);
-        v[it][0].load(vp + d0);
-        v[it][1].load(vp + d1);
-        x[0].get(k[it]);
-        x[1].get(k[it] + 8);
+        kr[it][0].load(kp + d0);
+        kr[it][1].load(kp + d1);
+        vr[it][0].load(vp + d0);
+        vr[it][1].load(vp + d1);
+      }
+  };
+  load(g0);
+  for (int head = g0; head < g1; ++head) {
+    float k[NIT][16], mk = 0.f, mv = 0.f;
+    Vec8<T> v[NIT][2];
+#pragma unroll
+    for (int it = 0; it < NIT; ++it)
+      if (row[it] < nr) {
+        kr[it][0].get(k[it]);
+        kr[it][1].get(k[it] + 8);
         if (turned) rotate16(k[it], cs[it], sn[it], neighbour);
         float y[16];
+        v[it][0] = vr[it][0];
+        v[it][1] = vr[it][1];
         v[it][0].get(y);
         v[it][1].get(y + 8);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          mk = amax_finite(mk, k[it][i]);
-          mv = amax_finite(mv, y[i]);
+          mk = fmaxf(mk, fabsf(k[it][i]));  // a NaN leaves the maximum as it is
+          mv = fmaxf(mv, fabsf(y[i]));
         }
       }
+    if (head + 1 < g1) load(head + 1);
     const int64_t si = (int64_t)page * a.c.hkv + head;
     float k_was = 0.f, v_was = 0.f;
-    if (page_ok && slot0 > 0) k_was = a.c.ks[si], v_was = a.c.vs[si];
-    mk = warp_max(mk);
-    mv = warp_max(mv);
-    if ((tid & 31) == 0) red[g & 1][0][tid >> 5] = mk, red[g & 1][1][tid >> 5] = mv;
-    __syncthreads();  // also orders every read of the old scales before their update
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-      mk = fmaxf(mk, red[g & 1][0][w]);
-      mv = fmaxf(mv, red[g & 1][1][w]);
-    }
-    if (page_ok) {
-      const float k_now = fmaxf(k_was, pow2(scale_exponent(mk))), v_now = fmaxf(v_was, pow2(scale_exponent(mv)));
-      if (tid == 0) a.c.ks[si] = k_now, a.c.vs[si] = v_now;
-      uint8_t* kp = a.c.k + si * ps * D;
-      uint8_t* vp = a.c.v + si * ps * D;
-      if (slot0 > 0 && k_now > k_was) rescale_rows(kp, slot0 * D, k_was / k_now);
-      if (slot0 > 0 && v_now > v_was) rescale_rows(vp, slot0 * D, v_was / v_now);
-      const float ik = 1.f / k_now, iv = 1.f / v_now;
+    if (slot0 > 0) k_was = a.c.ks[si], v_was = a.c.vs[si];
+    block_max(red[0], mk, mv);  // its barrier also orders every read of the old scales before their update
+    if (mk == INFINITY || mv == INFINITY) {  // rare: once more without the infinities
+      mk = mv = 0.f;
 #pragma unroll
       for (int it = 0; it < NIT; ++it)
         if (row[it] < nr) {
-          const int at = (slot0 + row[it]) * D;
-          store_codes(kp + at + d0, k[it], ik);
-          store_codes(kp + at + d1, k[it] + 8, ik);
           float y[16];
           v[it][0].get(y);
           v[it][1].get(y + 8);
-          store_codes(vp + at + d0, y, iv);
-          store_codes(vp + at + d1, y + 8, iv);
-        }
-    }
-    for (int h = head * a.gs; h < (head + 1) * a.gs; ++h)
 #pragma unroll
-      for (int it = 0; it < NIT; ++it)
-        if (row[it] < nr) {
-          const T* qp = static_cast<const T*>(a.q) + (row0 + row[it]) * a.qs + (int64_t)h * D;
-          T* op = static_cast<T*>(a.q_out) + (row0 + row[it]) * a.qos + (int64_t)h * D;
-          Vec8<T> x[2];
-          float y[16];
-          x[0].load(qp + d0);
-          x[1].load(qp + d1);
-          x[0].get(y);
-          x[1].get(y + 8);
-          if (turned) rotate16(y, cs[it], sn[it], neighbour);
-          Vec8<T>::store(op + d0, y);
-          Vec8<T>::store(op + d1, y + 8);
+          for (int i = 0; i < 16; ++i) {
+            mk = amax_finite(mk, k[it][i]);
+            mv = amax_finite(mv, y[i]);
+          }
         }
+      block_max(red[1], mk, mv);
+    }
+    const float k_now = fmaxf(k_was, pow2(scale_exponent(mk))), v_now = fmaxf(v_was, pow2(scale_exponent(mv)));
+    if (tid == 0) a.c.ks[si] = k_now, a.c.vs[si] = v_now;
+    uint8_t* kp = a.c.k + si * ps * D;
+    uint8_t* vp = a.c.v + si * ps * D;
+    if (slot0 > 0 && k_now > k_was) rescale_rows(kp, slot0 * D, k_was / k_now, tid, blockDim.x);
+    if (slot0 > 0 && v_now > v_was) rescale_rows(vp, slot0 * D, v_was / v_now, tid, blockDim.x);
+    const float ik = 1.f / k_now, iv = 1.f / v_now;
+#pragma unroll
+    for (int it = 0; it < NIT; ++it)
+      if (row[it] < nr) {
+        const int at = (slot0 + row[it]) * D;
+        store_codes(kp + at + d0, k[it], ik);
+        store_codes(kp + at + d1, k[it] + 8, ik);
+        float y[16];
+        v[it][0].get(y);
+        v[it][1].get(y + 8);
+        store_codes(vp + at + d0, y, iv);
+        store_codes(vp + at + d1, y + 8, iv);
+      }
+    __syncthreads();  // red is used again
   }
+  if (ROLE == kKeysValues) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <typename T, int D>
-cudaError_t launch_append(const AppendArgs& a, int blocks, int units, cudaStream_t s) {
-  const int nit = units > 256 ? 2 : 1;
+cudaError_t launch_append(const AppendArgs& a, int64_t pages, int units, bool split, cudaStream_t s) {
+  const int nit = units > 512 ? 2 : 1;
   const int threads = ((units + nit - 1) / nit + 31) / 32 * 32;
-  if (nit == 2)
-    append_kernel<T, D, 2><<<blocks, threads, 0, s>>>(a);
-  else
-    append_kernel<T, D, 1><<<blocks, threads, 0, s>>>(a);
-  return cudaGetLastError();
+  if (!split) {
+    const int blocks = (int)(pages * (a.kv_blocks + a.q_blocks));
+    if (nit == 2)
+      append_kernel<T, D, 2, kBoth><<<blocks, threads, 0, s>>>(a);
+    else
+      append_kernel<T, D, 1, kBoth><<<blocks, threads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  append_kernel<T, D, 1, kQueries><<<(int)(pages * a.q_blocks), threads < 256 ? threads : 256, 0, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((int)(pages * a.kv_blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return nit == 2 ? cudaLaunchKernelEx(&cfg, append_kernel<T, D, 2, kKeysValues>, a)
+                  : cudaLaunchKernelEx(&cfg, append_kernel<T, D, 1, kKeysValues>, a);
 }
 
 // ------------------------------------------------------------------ attention
@@ -813,20 +925,30 @@ extern "C" int dec_kv_append(const dec_paged_cache* cache, const dec_rope* rope,
 
   const int ps = cache->page_size;
   if (max_new > n_tokens) max_new = n_tokens;  // no valid sequence has more
-  AppendArgs a{device_cache(cache), rope->inv_freq, rope->rot_dim, rope->pairs == DEC_ROPE_NEIGHBOUR, rope->factor, q, k,
-               v, q_out, q_stride, k_stride, v_stride, q_out_stride, q ? n_heads / hkv : 0, n_tokens, max_new,
-               (int)(((int64_t)max_new + ps - 2) / ps + 1), 1, cu_new, seq_lens, page_table, table_stride, status};
-  const int64_t blocks = (int64_t)n_seqs * a.pieces * (hkv / a.hpc);
-  if (blocks > INT32_MAX) return DEC_ERR_UNSUPPORTED;
+  const int64_t pieces = ((int64_t)max_new + ps - 2) / ps + 1, pages = n_seqs * pieces;
   const int units = (max_new < ps ? max_new : ps) * (D / 16);
+  AppendArgs a{device_cache(cache), rope->inv_freq, rope->rot_dim, rope->pairs == DEC_ROPE_NEIGHBOUR, rope->factor, q, k,
+               v, q_out, q_stride, k_stride, v_stride, q_out_stride, q ? n_heads : 0, n_tokens, max_new, (int)pieces,
+               hkv, q ? hkv : 0, cu_new, seq_lens, page_table, table_stride, status};
+  // A block a kv head, and one for its query heads, is the shortest path for few tokens; more blocks than fill the GPU
+  // compute the angles over and over.  With blocks that a page fills (256 threads or more) twice the SMs are enough
+  // and queries and keys are launches of their own, each with the registers it needs; with little in each, 8 an SM.  B200,
+  // 32 / 8 heads of 128, us, one way and the other: 256 single tokens 7.1 (8 an SM) / 9.9 (2), 8 x 1000 tokens 50.3 / 41.6,
+  // 4 x 8192 154 (one launch) / 138 (two), 64 x 4 tokens 5.0 / 9.8.
+  const bool split = q && units >= 256;
+  const int64_t enough = split ? 2 * 148 : 8 * 148;
+  while (a.kv_blocks > 1 && pages * a.kv_blocks > enough) a.kv_blocks = (a.kv_blocks + 1) / 2;
+  while (a.q_blocks > 1 && pages * a.q_blocks > enough) a.q_blocks = (a.q_blocks + 1) / 2;
+  const int64_t blocks = pages * (a.kv_blocks + a.q_blocks);
+  if (pages > INT32_MAX || blocks > INT32_MAX) return DEC_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == DEC_BF16)
-    e = D == 64 ? launch_append<__nv_bfloat16, 64>(a, (int)blocks, units, st)
-                : launch_append<__nv_bfloat16, 128>(a, (int)blocks, units, st);
+    e = D == 64 ? launch_append<__nv_bfloat16, 64>(a, pages, units, split, st)
+                : launch_append<__nv_bfloat16, 128>(a, pages, units, split, st);
   else
-    e = D == 64 ? launch_append<float, 64>(a, (int)blocks, units, st)
-                : launch_append<float, 128>(a, (int)blocks, units, st);
+    e = D == 64 ? launch_append<float, 64>(a, pages, units, split, st)
+                : launch_append<float, 128>(a, pages, units, split, st);
   return e == cudaSuccess ? DEC_OK : DEC_ERR_CUDA;
 }
 
