@@ -2,7 +2,12 @@
 #include <cuda_fp16.h>
 #include <float.h>
 
+#include <random>
+
 #include "op_common.cuh"
+#ifndef LEAST
+#define LEAST 2
+#endif
 
 namespace {
 
@@ -337,9 +342,10 @@ cudaError_t launch_append(const AppendArgs& a, int64_t pages, int units, bool sp
 
 // ------------------------------------------------------------------ attention
 // The batch is one line of tiles: (sequence, kv head, 16 positions), sequences in order.  It is cut into equal
-// contiguous pieces, one a warp, so a GPU full of warps is busy whatever the lengths are, and what a warp, a block
-// and the grid leave unfinished at their two ends is joined by log-sum-exp: warps of a block in shared memory, blocks
-// in a second small kernel.
+// contiguous pieces, one a warp, so a GPU full of warps is busy whatever the lengths are, and what warps and blocks
+// leave unfinished at their two ends is joined by log-sum-exp: a block's warps in shared memory, and blocks by the one in
+// which the (sequence, head) ends, which waits for those before it.  (They were dispatched before it and wait for none
+// behind them, so it never waits for a block that has no SM.)  Sums are in the order of the line: the same bits every time.
 //
 // A warp computes S^T = K q^T (16 positions x 8 query heads) and O^T += V^T P (D x 8) with m16n8k16 fp16 MMAs.
 // E4M3 codes are exact in fp16; q is scaled by a power of two into fp16's upper range, where a bf16 q is exact; the
@@ -355,6 +361,7 @@ cudaError_t launch_append(const AppendArgs& a, int64_t pages, int units, bool sp
 constexpr int kBlocks = 148;  // one block per SM of a B200
 constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
+constexpr int kLeast = LEAST;  // tiles a warp has at least, before another block is taken
 
 struct PagedArgs {
   Cache c;
@@ -365,8 +372,9 @@ struct PagedArgs {
   const int32_t *lens, *table;
   int table_stride;
   float scale_log2;
-  float* part;  // [kBlocks][2] open ends: m[8], m'[8], l[8], O[8][D]
-  int4* meta;   // [kBlocks][2] {sequence, head, ends at the sequence's end, in use}
+  float* part;     // [kBlocks][2] open ends (0: that began before the block, 1: that begins in it): m[8], m'[8], l[8], O[8][D]
+  uint64_t* ready; // [kBlocks][2] `key` once part is written; whoever reads it clears it
+  uint64_t key;    // what `ready` holds then: a number of this process that uninitialised memory does not hold
   int32_t* status;
 };
 
@@ -380,6 +388,7 @@ struct Place {
   int s, head, tile, tiles, len;
   __device__ __forceinline__ void enter(const PagedArgs& a) {  // the first sequence from s on that has tiles
     tiles = 0;
+#pragma unroll 1
     while (s < a.n_seqs && (tiles = tiles_of(a, s)) == 0) ++s;
     len = tiles ? a.lens[s] : 0;
   }
@@ -441,7 +450,7 @@ struct PagedShape {
   static constexpr int kSlot = (24 + 8 * D) * 4;    // m[8], m'[8], l[8], O[8][D]
   static constexpr int kRing = kStages * kStage;    // also holds a warp's last open end once its copies are done
   static constexpr int kSmem = kWarps * (kRing + kSlot);
-  static_assert(kRing >= kSlot && kSmem <= 227 * 1024 - 8192, "shared memory");
+  static_assert(kRing >= kSlot && kSmem <= 227 * 1024 - 24 * 1024, "shared memory");
 };
 
 // Weights of an open end in a join: 2^(m - M), nothing where the end saw no position.
@@ -452,6 +461,28 @@ __device__ __forceinline__ float unit(float l, float M, float Mp) {
   return l == 0.f ? 0.f : ex2(Mp - M - 4.f) / l;
 }
 
+__device__ __forceinline__ uint64_t clock_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ uint64_t load_acquire(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_release(uint64_t* p, uint64_t v) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+
+__device__ __forceinline__ void store4(float* p, float x, float y, float z, float w) {
+  *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float x, float y, float z, float w) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x, y), b = __floats2bfloat162_rn(z, w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
   using Sh = PagedShape<D>;
@@ -460,66 +491,85 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
   constexpr int kRow = D / 64;              // 16-byte chunks of a K row a lane reads
   constexpr int kPer = Sh::kTile / 512;     // 16-byte copies a lane issues for K, and for V
   extern __shared__ __align__(16) uint8_t sm[];
-  __shared__ long long before[kThreads];
-  __shared__ long long warp_sum_s[kWarps];
-  __shared__ int4 open_meta[kWarps][2];
+  __shared__ unsigned before[kThreads], warp_sum_s[kWarps];
+  __shared__ int4 open_s[2 * kWarps];
+  __shared__ int late_s, list_s[2 * kWarps];
+  __shared__ float m_s[kBlocks + 2 * kWarps][8], mp_s[kBlocks + 2 * kWarps][8], l_s[kBlocks + 2 * kWarps][8], tot_s[3][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;");
 
   // ---- where this warp's piece of the line is
-  const int per = (a.n_seqs + kThreads - 1) / kThreads;
-  long long mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int s = tid * per + i;
-    if (s < a.n_seqs) mine += tiles_of(a, s);
-  }
-  long long scan = mine;
+  if (lane < 2) open_s[2 * warp + lane] = make_int4(-1, -1, 0, 0);
+  if (tid == 0) late_s = 0;
+  const int gw = blockIdx.x * kWarps + warp;
+  const int per = a.n_seqs <= 32 ? 1 : (a.n_seqs + kThreads - 1) / kThreads;  // sequences a lane, or a thread, counts
+  const int s0 = (a.n_seqs <= 32 ? lane : tid) * per;
+  unsigned mine = 0;  // the host has seen to it that 32 bits are enough
+#pragma unroll 1
+  for (int i = 0; i < per; ++i)
+    if (s0 + i < a.n_seqs) mine += tiles_of(a, s0 + i);
+  mine *= a.c.hkv;
+  unsigned scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, scan, o);
+    const unsigned y = __shfl_up_sync(0xffffffffu, scan, o);
     if (lane >= o) scan += y;
   }
-  if (lane == 31) warp_sum_s[warp] = scan;
-  if (lane < 2) open_meta[warp][lane] = make_int4(-1, 0, 0, 0);
-  __syncthreads();
-  long long total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) scan += total;
-    total += warp_sum_s[w];
+  unsigned total = __shfl_sync(0xffffffffu, scan, 31);
+  if (a.n_seqs > 32) {  // up to 32 every warp counts for itself
+    if (lane == 31) warp_sum_s[warp] = scan;
+    __syncthreads();
+    total = 0;
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) scan += total;
+      total += warp_sum_s[w];
+    }
+    before[tid] = scan - mine;
+    __syncthreads();
   }
-  before[tid] = scan - mine;
-  __syncthreads();
-  const int gw = blockIdx.x * kWarps + warp;
+#pragma unroll 1
   for (int s = gw; s < a.n_seqs; s += kBlocks * kWarps) {  // sequences without positions
     if (tiles_of(a, s) == 0) {
       if (lane == 0 && a.lens[s] != 0) flag(a.status, DEC_SEQ_BAD_RANGE);
+#pragma unroll 1
       for (int e = lane * 8; e < a.gs * a.c.hkv * D; e += 256) {
         const float z[8] = {};
         Vec8<T>::store(static_cast<T*>(a.out) + s * a.os + e, z);
       }
     }
   }
-  total *= a.c.hkv;
-  const long long begin = total * gw / (kBlocks * kWarps), end = total * (gw + 1) / (kBlocks * kWarps);
-  int left = (int)(end - begin);
+  // the first `more` warps have each + 1 tiles, the others `each`
+  const unsigned blocks = min((total + kLeast * kWarps - 1) / (kLeast * kWarps), (unsigned)kBlocks);
+  if (blockIdx.x >= blocks) return;
+  const unsigned warps = blocks * kWarps, each = total / warps, more = total - each * warps;
+  const unsigned begin = gw * each + min((unsigned)gw, more);
+  int left = (int)(each + (gw < more));
   Place get;
   if (left > 0) {
-    int lo = 0, hi = kThreads - 1;  // the last thread whose sequences begin at or before `begin`
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (before[mid] * a.c.hkv <= begin) lo = mid; else hi = mid - 1;
+    unsigned at = 0;  // where the sequence begins on the line
+    if (a.n_seqs <= 32) {
+      get.s = __ffs(__ballot_sync(0xffffffffu, scan > begin)) - 1;
+      at = __shfl_sync(0xffffffffu, scan - mine, get.s);
+    } else {
+      int lo = 0, hi = kThreads - 1;  // the last thread whose sequences begin at or before `begin`
+#pragma unroll 1
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] <= begin) lo = mid; else hi = mid - 1;
+      }
+      at = before[lo];
+      get.s = lo * per;
     }
-    long long at = before[lo] * a.c.hkv;
-    get.s = lo * per;
     get.enter(a);
-    while (get.s < a.n_seqs && at + (long long)get.tiles * a.c.hkv <= begin) {
-      at += (long long)get.tiles * a.c.hkv;
+#pragma unroll 1
+    while (get.s < a.n_seqs && at + (unsigned)(get.tiles * a.c.hkv) <= begin) {
+      at += get.tiles * a.c.hkv;
       ++get.s;
       get.enter(a);
     }
     if (get.s < a.n_seqs) {
-      get.head = (int)((begin - at) / get.tiles);
-      get.tile = (int)((begin - at) % get.tiles);
+      get.head = (begin - at) / (unsigned)get.tiles;
+      get.tile = (begin - at) - get.head * get.tiles;
     } else {
       left = 0;  // the lengths changed under the call
     }
@@ -565,10 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   look_up();
+#pragma unroll 1
   for (int i = 0; i < Sh::kStages - 1; ++i) fetch();
 
   // ---- one (sequence, kv head) after another
   int stage = 0;
+  unsigned at_tile = begin;  // the segment's first tile on the line
   while (left > 0) {
     uint32_t qh[kSteps][2], ql[kPair ? kSteps : 1][2];
     float f0, f1;  // score factors of this lane's two heads, 2t and 2t + 1
@@ -612,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
     float o[kSteps][4] = {}, m0 = -INFINITY, m1 = -INFINITY, n0 = -INFINITY, n1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     int count = min(left, tiles - tile0);
     const bool whole_end = tile0 + count == tiles;
+    const int counted = count;
     left -= count;
     for (; count > 0; --count) {
       asm volatile("cp.async.wait_group %0;" ::"n"(Sh::kStages - 2) : "memory");
@@ -717,7 +770,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
         __syncwarp();
         to = reinterpret_cast<float*>(ring);
       }
-      if (lane == 0) open_meta[warp][which] = make_int4(s, head, (tile0 == 0) | (whole_end ? 2 : 0), 1);
+      if (lane == 0) {
+        int first = blockIdx.x;  // the block in which this (sequence, head) begins
+        if (tile0 > 0) {
+          const unsigned t0 = at_tile - tile0, edge = more * (each + 1);
+          first = (int)((t0 < edge ? t0 / (each + 1) : more + (t0 - edge) / each) / kWarps);
+        }
+        open_s[2 * warp + which] = make_int4(s, head, (tile0 == 0) | (whole_end ? 2 : 0), first);
+      }
       if (g == 0) {
         to[2 * t] = m0, to[2 * t + 1] = m1, to[8 + 2 * t] = n0, to[8 + 2 * t + 1] = n1;
         to[16 + 2 * t] = l0, to[16 + 2 * t + 1] = l1;
@@ -729,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
         *reinterpret_cast<float2*>(to + 24 + (2 * t + 1) * D + d) = make_float2(o[i][1], o[i][3]);
       }
     }
-    // on to the next (sequence, head); `use` is at this one's first tile here
+    at_tile += counted;
     use.tile = tiles - 1;
     if (left > 0) use.next(a);
     if (use.s >= a.n_seqs) left = 0;
@@ -737,112 +797,144 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
 
-  // ---- join what the warps left open; what stays open goes to the second kernel
-  int4* meta = a.meta + 2 * blockIdx.x;
-  bool used[2] = {false, false};
-  for (int i = 0; i < 2 * kWarps;) {
-    const int4 mi = open_meta[i >> 1][i & 1];
-    if (!mi.w) {
-      ++i;
-      continue;
-    }
-    int j = i, flags = mi.z;
-    bool closed = flags & 2;
-    int n = i + 1;
-    for (; n < 2 * kWarps && !closed; ++n) {
-      const int4 mn = open_meta[n >> 1][n & 1];
-      if (!mn.w) continue;
-      if (mn.x != mi.x || mn.y != mi.y) break;
-      closed = mn.z & 2;
-    }
-    const bool whole = (flags & 1) && closed;
-    const int which = flags & 1;
-    float* part = a.part + (size_t)(2 * blockIdx.x + which) * (24 + 8 * D);
-    for (int e = tid; e < 8 * (D / 4); e += kThreads) {
-      const int h = e / (D / 4), d = e % (D / 4) * 4;
-      float M = -INFINITY, Mp = -INFINITY;
-      for (int k = j; k < n; ++k)
-        if (open_meta[k >> 1][k & 1].w) {
-          const float* p = k & 1 ? reinterpret_cast<float*>(sm + (k >> 1) * Sh::kRing)
-                                 : reinterpret_cast<float*>(sm + kWarps * Sh::kRing + (k >> 1) * Sh::kSlot);
-          M = fmaxf(M, p[h]);
-          Mp = fmaxf(Mp, p[8 + h]);
+  // ---- join what the warps left open: runs of slots of one (sequence, head)
+  const int4 mine_o = lane < 2 * kWarps ? open_s[lane] : make_int4(-1, -1, 0, 0);
+  const uint32_t used = __ballot_sync(0xffffffffu, mine_o.x >= 0);
+  const uint32_t below = used & ((1u << lane) - 1);
+  const int prev = below ? 31 - __clz(below) : 0;
+  const int px = __shfl_sync(0xffffffffu, mine_o.x, prev), py = __shfl_sync(0xffffffffu, mine_o.y, prev);
+  uint32_t starts = __ballot_sync(0xffffffffu, mine_o.x >= 0 && (!below || px != mine_o.x || py != mine_o.y));
+  if (!starts) return;
+  auto slot_at = [&](int k) {
+    return k & 1 ? reinterpret_cast<const float*>(sm + (k >> 1) * Sh::kRing)
+                 : reinterpret_cast<const float*>(sm + kWarps * Sh::kRing + (k >> 1) * Sh::kSlot);
+  };
+  constexpr int kItems = 8 * (D / 4);  // (head, four dims)
+  // Short runs first, a warp each; then long ones, by all warps; last the one that waits for earlier blocks, so that what
+  // a block hands on never waits for what it is handed.
+  for (int pass = 0; pass < 3; ++pass) {
+    uint32_t todo = starts;
+    for (int run = 0; todo; ++run) {
+      const int i0 = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const uint32_t members = used & ~((1u << i0) - 1) & (todo ? (1u << (__ffs(todo) - 1)) - 1 : 0xFFFFFFFFu);
+      const int4 fst = open_s[i0], lst = open_s[31 - __clz(members)];
+      const bool from_start = fst.z & 1, to_end = lst.z & 2, waits = !from_start && to_end;
+      const int first = waits ? fst.w : blockIdx.x, local = __popc(members);  // blocks first .. this one - 1 have parts of it
+      const bool shorter = !waits && local <= 4;
+      if (pass != (waits ? 2 : shorter ? 0 : 1) || (shorter && run % kWarps != warp)) continue;
+      float* part = a.part + (size_t)(2 * blockIdx.x + from_start) * (24 + 8 * D);
+      auto put = [&](int h, int d, const float (&x)[4], float M, float Mp, float l) {
+        if (to_end) {
+          if (h < a.gs) {
+            const float u = unit(l, M, Mp);
+            T* op = static_cast<T*>(a.out) + fst.x * a.os + ((int64_t)fst.y * a.gs + h) * D + d;
+            store4(op, x[0] * u, x[1] * u, x[2] * u, x[3] * u);
+          }
+        } else {
+          if (d == 0) part[h] = M, part[8 + h] = Mp, part[16 + h] = l;
+          *reinterpret_cast<float4*>(part + 24 + h * D + d) = make_float4(x[0], x[1], x[2], x[3]);
         }
-      float l = 0.f, x[4] = {};
-      for (int k = j; k < n; ++k)
-        if (open_meta[k >> 1][k & 1].w) {
-          const float* p = k & 1 ? reinterpret_cast<float*>(sm + (k >> 1) * Sh::kRing)
-                                 : reinterpret_cast<float*>(sm + kWarps * Sh::kRing + (k >> 1) * Sh::kSlot);
-          l = fmaf(p[16 + h], join_weight(p[h], M), l);
-          const float w = join_weight(p[8 + h], Mp);
-          const float4 y = *reinterpret_cast<const float4*>(p + 24 + h * D + d);
-          x[0] = fmaf(y.x, w, x[0]), x[1] = fmaf(y.y, w, x[1]), x[2] = fmaf(y.z, w, x[2]), x[3] = fmaf(y.w, w, x[3]);
+      };
+      if (shorter) {
+        const float* at[4];  // an end that is not there weighs nothing
+        int own = 0;
+        uint32_t left_m = members;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          at[k] = slot_at(left_m ? __ffs(left_m) - 1 : i0);
+          left_m &= left_m - 1;
+          if (k == lane >> 3) own = k;
         }
-      if (whole) {
-        if (h < a.gs) {
-          const float u = unit(l, M, Mp);
-          T* op = static_cast<T*>(a.out) + mi.x * a.os + ((int64_t)mi.y * a.gs + h) * D + d;
-          for (int k = 0; k < 4; ++k) op[k] = (T)(x[k] * u);
+        // lane (k, h): end k's weights for head h
+        const float* p = own & 2 ? (own & 1 ? at[3] : at[2]) : (own & 1 ? at[1] : at[0]);
+        const int hl = lane & 7;
+        const bool there = own < local;
+        const float m = there ? p[hl] : -INFINITY, mp = there ? p[8 + hl] : -INFINITY;
+        float M = m, Mp = mp;
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) {
+          M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          Mp = fmaxf(Mp, __shfl_xor_sync(0xffffffffu, Mp, o));
         }
+        const float v = join_weight(mp, Mp);
+        float l = there ? p[16 + hl] * join_weight(m, M) : 0.f;
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll 2
+        for (int it = 0; it < kItems / 32; ++it) {
+          const int h = (lane + 32 * it) / (D / 4), d = (lane + 32 * it) % (D / 4) * 4;
+          float x[4] = {};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float vk = __shfl_sync(0xffffffffu, v, 8 * k + h);
+            if (k < local) {
+              const float4 y = *reinterpret_cast<const float4*>(at[k] + 24 + h * D + d);
+              x[0] = fmaf(y.x, vk, x[0]), x[1] = fmaf(y.y, vk, x[1]), x[2] = fmaf(y.z, vk, x[2]), x[3] = fmaf(y.w, vk, x[3]);
+            }
+          }
+          put(h, d, x, __shfl_sync(0xffffffffu, M, h), __shfl_sync(0xffffffffu, Mp, h), __shfl_sync(0xffffffffu, l, h));
+        }
+        __syncwarp();
       } else {
-        if (d == 0) part[h] = M, part[8 + h] = Mp, part[16 + h] = l;
-        *reinterpret_cast<float4*>(part + 24 + h * D + d) = make_float4(x[0], x[1], x[2], x[3]);
+        const int remote = blockIdx.x - first, n = remote + local;
+        auto remote_at = [&](int k) { return a.part + (size_t)(2 * (first + k) + (k == 0)) * (24 + 8 * D); };
+        for (int k = tid; k < remote; k += kThreads) {  // the earlier blocks' parts have to be there
+          const uint64_t* r = a.ready + 2 * (first + k) + (k == 0);
+          const uint64_t t0 = clock_ns();
+          while (load_acquire(r) != a.key)
+            if (clock_ns() - t0 > 1000000000ull) {
+              late_s = 1;
+              break;
+            }
+        }
+        if (warp == 0 && members >> lane & 1) list_s[__popc(members & ((1u << lane) - 1))] = lane;
+        __syncthreads();
+        for (int e = tid; e < n * 8; e += kThreads) {
+          const int k = e >> 3, h = e & 7;
+          const float* p = k < remote ? remote_at(k) : slot_at(list_s[k - remote]);
+          m_s[k][h] = p[h], mp_s[k][h] = p[8 + h], l_s[k][h] = p[16 + h];
+        }
+        __syncthreads();
+        if (warp < 8) {  // a head's maxima, sum and weights
+          const int h = warp;
+          float M = -INFINITY, Mp = -INFINITY, l = 0.f;
+          for (int k = lane; k < n; k += 32) M = fmaxf(M, m_s[k][h]), Mp = fmaxf(Mp, mp_s[k][h]);
+          M = warp_max(M), Mp = warp_max(Mp);
+          for (int k = lane; k < n; k += 32) {
+            l = fmaf(l_s[k][h], join_weight(m_s[k][h], M), l);
+            mp_s[k][h] = join_weight(mp_s[k][h], Mp);
+          }
+          l = warp_sum(l);
+          if (lane == 0) tot_s[0][h] = M, tot_s[1][h] = Mp, tot_s[2][h] = l;
+        }
+        __syncthreads();
+        for (int e = tid; e < kItems; e += kThreads) {
+          const int h = e / (D / 4), d = e % (D / 4) * 4;
+          float x[4] = {};
+#pragma unroll 8
+          for (int k = 0; k < remote; ++k) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(remote_at(k) + 24 + h * D + d));
+            const float v = mp_s[k][h];
+            x[0] = fmaf(y.x, v, x[0]), x[1] = fmaf(y.y, v, x[1]), x[2] = fmaf(y.z, v, x[2]), x[3] = fmaf(y.w, v, x[3]);
+          }
+#pragma unroll 2
+          for (int k = 0; k < local; ++k) {
+            const float4 y = *reinterpret_cast<const float4*>(slot_at(list_s[k]) + 24 + h * D + d);
+            const float v = mp_s[remote + k][h];
+            x[0] = fmaf(y.x, v, x[0]), x[1] = fmaf(y.y, v, x[1]), x[2] = fmaf(y.z, v, x[2]), x[3] = fmaf(y.w, v, x[3]);
+          }
+          put(h, d, x, tot_s[0][h], tot_s[1][h], tot_s[2][h]);
+        }
+        __syncthreads();
+        for (int k = tid; k < remote; k += kThreads) a.ready[2 * (first + k) + (k == 0)] = 0;  // read: for the next call
+        if (tid == 0 && late_s) flag(a.status, DEC_SEQ_TIMEOUT);
+      }
+      if (!to_end && (shorter ? lane == 0 : tid == 0)) {
+        __threadfence();
+        store_release(a.ready + 2 * blockIdx.x + from_start, a.key);
       }
     }
-    if (!whole) {
-      used[which] = true;
-      if (tid == 0) meta[which] = make_int4(mi.x, mi.y, closed, 1);
-    }
-    i = n;
-  }
-  if (tid < 2 && !used[tid]) meta[tid] = make_int4(-1, 0, 0, 0);
-}
-
-// Block b joins the (sequence, head) that begins in block b of the first kernel and goes on behind it: its slot 1
-// and the slots 0 of the blocks that follow, up to the one that ends it.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) paged_join(PagedArgs a) {
-  __shared__ int last_s, used_s[kBlocks];
-  __shared__ float M_s[8], Mp_s[8], u_s[8];
-  const int tid = threadIdx.x, b = blockIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 me = a.meta[2 * b + 1];
-  if (!me.w) return;
-  if (tid == 0) last_s = kBlocks - 1;
-  __syncthreads();
-  if (tid >= b && tid < kBlocks) {
-    const int4 m = tid == b ? me : a.meta[2 * tid];
-    used_s[tid] = m.w;
-    if (m.w && m.z) atomicMin(&last_s, tid);  // the first end behind b is ours
-  }
-  __syncthreads();
-  const int last = last_s;
-  auto part = [&](int i) { return a.part + (size_t)(i == b ? 2 * b + 1 : 2 * i) * (24 + 8 * D); };
-  const int warp = tid >> 5, lane = tid & 31;
-  {  // warp h: head h's maxima and sum
-    float M = -INFINITY, Mp = -INFINITY, l = 0.f;
-    for (int i = b + lane; i <= last; i += 32)
-      if (used_s[i]) M = fmaxf(M, part(i)[warp]), Mp = fmaxf(Mp, part(i)[8 + warp]);
-    M = warp_max(M), Mp = warp_max(Mp);
-    for (int i = b + lane; i <= last; i += 32)
-      if (used_s[i]) l = fmaf(part(i)[16 + warp], join_weight(part(i)[warp], M), l);
-    l = warp_sum(l);
-    if (lane == 0) Mp_s[warp] = Mp, u_s[warp] = unit(l, M, Mp);
-  }
-  __syncthreads();
-  for (int e = tid; e < a.gs * (D / 4); e += 256) {
-    const int h = e / (D / 4), d = e % (D / 4) * 4;
-    const float Mp = Mp_s[h];
-    float x[4] = {};
-#pragma unroll 4
-    for (int i = b; i <= last; ++i) {
-      if (!used_s[i]) continue;
-      const float w = join_weight(part(i)[8 + h], Mp);
-      const float4 y = *reinterpret_cast<const float4*>(part(i) + 24 + h * D + d);
-      x[0] = fmaf(y.x, w, x[0]), x[1] = fmaf(y.y, w, x[1]), x[2] = fmaf(y.z, w, x[2]), x[3] = fmaf(y.w, w, x[3]);
-    }
-    T* op = static_cast<T*>(a.out) + me.x * a.os + ((int64_t)me.y * a.gs + h) * D + d;
-    for (int j = 0; j < 4; ++j) op[j] = (T)(x[j] * u_s[h]);
   }
 }
 
@@ -853,18 +945,7 @@ cudaError_t launch_paged(const PagedArgs& a, cudaStream_t s) {
       cudaFuncSetAttribute(paged_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
   if (e != cudaSuccess) return e;
   paged_kernel<T, D><<<kBlocks, kThreads, Sh::kSmem, s>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kBlocks);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at;  // the join's blocks wait on the GPU for the first kernel's end, not in the queue
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join<T, D>, a);
+  return cudaGetLastError();
 }
 
 int check_cache(const dec_paged_cache* c) {
@@ -959,7 +1040,7 @@ extern "C" int dec_attention_paged_workspace(const dec_paged_cache* cache, int32
   if (rc) return rc;
   rc = head_layout(n_heads, cache->n_kv_heads, cache->head_dim);
   if (rc) return rc;
-  *out_bytes = kBlocks * 2 * (sizeof(int4) + (24 + 8 * (size_t)cache->head_dim) * sizeof(float));
+  *out_bytes = kBlocks * 2 * (sizeof(uint64_t) + (24 + 8 * (size_t)cache->head_dim) * sizeof(float));
   return DEC_OK;
 }
 
@@ -986,10 +1067,15 @@ extern "C" int dec_attention_paged(const dec_paged_cache* cache, int32_t dtype, 
   if (!cache_on_device(cache, dev) || !on_device(q, dev) || !on_device(out, dev) || !on_device(workspace, dev) ||
       !on_device(seq_lens, dev) || !on_device(page_table, dev) || (status && !on_device(status, dev)))
     return DEC_ERR_INVALID_ARG;
-  const size_t meta = kBlocks * 2 * sizeof(int4);
+  static const uint64_t key = [] {
+    std::random_device r;
+    return (uint64_t)r() << 32 | r() | 1;
+  }();
+  const size_t flags = kBlocks * 2 * sizeof(uint64_t);
+  if ((double)n_seqs * hkv * table_stride * cache->page_size / 16 >= 2147483648.0) return DEC_ERR_UNSUPPORTED;
   PagedArgs a{device_cache(cache), q, out, q_stride, out_stride, n_heads / hkv, n_seqs, 31 - __builtin_clz(cache->page_size),
               seq_lens, page_table, table_stride, scale * 1.4426950408889634f,
-              reinterpret_cast<float*>(static_cast<char*>(workspace) + meta), static_cast<int4*>(workspace), status};
+              reinterpret_cast<float*>(static_cast<char*>(workspace) + flags), static_cast<uint64_t*>(workspace), key, status};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == DEC_BF16)
