@@ -1,11 +1,10 @@
 // Attention of packed bf16 prompts on tcgen05 tensor cores.
 //
 // A block takes two tiles of 128 queries that read the same keys (two heads of one kv head, or neighbouring queries
-// of one head), and walks their keys 128 at a time:
-//   S = Q K^T (128 x 128, fp32 in TMEM), P = 2^(scale log2(e) S - m) rounded to bf16 over S, O += P V.
-// Warps 0-3 and 4-7 are the tiles' softmax, a thread a row; warp 8 issues every MMA; warp 9 every TMA load.  The softmax
-// keeps a row of S in registers: it takes them over from the last warpgroup (208 and 88 of the 168 at launch).
-//   TMEM: S0 | S1 (128 columns each, P in the first 64) | O0 | O1 (D columns each)
+// of one head), and walks their keys in steps of kN:
+//   S = Q K^T (128 x kN, fp32 in TMEM), P = 2^(scale log2(e) S - m) rounded to bf16 over S, O += P V.
+// Warps 0-3 and 4-7 are the tiles' softmax, a thread a row; warp 8 issues every MMA; warp 9 every TMA load.
+//   TMEM: S0 | S1 (kN columns each, P in the first kN / 2) | O0 | O1 (D columns each)
 //   shared memory: Q, and a ring of K and V tiles, rows of 128 bytes in the 128-byte swizzle
 // The tiles alternate: while one tile's softmax runs, the tensor cores do the other's P V and next Q K^T.
 // One thread's MMAs complete in the order they were issued.  So S_i(j + 1), issued behind P V_i(j), may overwrite P_i(j),
@@ -18,6 +17,13 @@
 // An unseen value meets a weight of zero, and zero times NaN or infinity is NaN.  Such values are rare and rows that have
 // met one show it, so it is looked for only in the results: a row that is not finite is computed once more with the keys
 // it sees alone (redo_row).
+//
+// What it measures: a causal 8k prompt, 32 heads of 128 on 8, 440-465 us, 1.18-1.25 PFLOP/s (72-76 % of cuBLAS's burst
+// rate); of heads of 64 325 us.  With the softmax left out the MMAs, loads and hand-overs take 395 us: the tensor cores wait
+// for hand-overs (about 800 cycles from S to P and on, two tiles to hide them) and for shared memory (Q K^T reads both
+// operands there at its full 128 bytes a cycle).  Tried and slower: two threads a row (115 against 100 us for six ragged
+// prompts of up to 1500, heads of 64; spills at 128), steps of 64 keys with two S buffers for heads of 128 (543), blocks that
+// stay for several pairs of tiles by a fixed plan (544: the plan's imbalance, and registers).
 #pragma once
 #include <cuda.h>
 
@@ -61,21 +67,28 @@ using dec::mbar_arrive;
 using dec::mbar_arrive_expect_tx;
 using dec::smem_u32;
 
-constexpr int kThreads = 384, kRegs = 168, kRegsSoftmax = 208, kRegsRest = 88;
-static_assert(256 * kRegsSoftmax + 128 * kRegsRest <= kThreads * kRegs, "registers handed over are those at launch");
-constexpr int kM = 128, kN = 128;
-#ifndef KPOLY
-#define KPOLY 3
-#endif
-constexpr int kPoly = KPOLY;  // of every 8 pairs of a row, those whose exponentials are the polynomial's
+constexpr int kM = 128;
+// Of every 8 pairs of a row's exponentials, those that the polynomial does.  8k causal prompt, 32 heads, us for 0 / 2 / 3 / 4:
+// heads of 128 492 / 465 / 469 / 530, of 64 337 / 325 / 328 / 362.
+constexpr int kPoly = 2;
 constexpr float kC0 = 0x1.fff692p-1f, kC1 = 0x1.62f31ap-1f, kC2 = 0x1.f0de1ap-3f, kC3 = 0x1.c3f75ep-5f;
 
+// Heads of 128: S and O of two tiles with steps of 128 keys fill an SM's TMEM, one block has the SM to itself, and its
+// softmax threads keep a row of S in registers that they take over from the last warpgroup.
+// Heads of 64: with steps of 64 keys they fill half of it, and two blocks share an SM (shared memory lets no third in):
+// four tiles whose waits overlap, as do one block's first loads and last stores with the other's steps.
 template <int D>
 struct Shape {
-  static constexpr int kTile = 128 * D * 2;  // bytes of 128 queries, keys or values
+  static constexpr int kN = D;                // keys of a step
+  static constexpr int kBlocks = 128 / D;     // on an SM
+  static constexpr int kColumns = 4 * D;      // of TMEM
+  static constexpr int kThreads = D == 128 ? 384 : 320;
+  static constexpr int kRegs = 168, kRegsSoftmax = 208, kRegsRest = 88;  // heads of 128: at launch, and handed over
+  static_assert(D != 128 || 256 * kRegsSoftmax + 128 * kRegsRest <= kThreads * kRegs, "those at launch");
+  static constexpr int kQ = kM * D * 2, kTile = kN * D * 2;  // bytes of a query tile, of a step's keys or values
   static constexpr int kStages = D == 128 ? 4 : 8;
-  static constexpr int kSmem = (2 + kStages) * kTile + 512;  // barriers behind the tiles; over half an SM's, so a block has
-                                                             // its SM, and all of its 512 TMEM columns, to itself
+  static constexpr int kSmem = 2 * kQ + kStages * kTile + 512;  // barriers behind the tiles
+  static_assert(kSmem <= 227 * 1024 / kBlocks - 1024 && kSmem > 227 * 1024 / (kBlocks + 1), "blocks on an SM");
 };
 
 struct Bars {
@@ -143,14 +156,21 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -216,6 +236,7 @@ __device__ __forceinline__ void redo_row(const PrefillArgs& a, const __nv_bfloat
     float s = -INFINITY;
     if (t < n) {
       s = 0.f;
+#pragma unroll 1
       for (int d = 0; d < D; d += 8) {
         Vec8<__nv_bfloat16> x, y;
         float u[8], w[8];
@@ -231,6 +252,7 @@ __device__ __forceinline__ void redo_row(const PrefillArgs& a, const __nv_bfloat
     const float p = t < n ? exp2f(s - base) : 0.f;
     l = l * f + warp_sum(p);
     for (int i = 0; i < kD; ++i) o[i] *= f;
+#pragma unroll 1
     for (int j = 0; j < 32 && t0 + j < n; ++j) {
       const float pj = __shfl_sync(0xffffffffu, p, j);
       for (int i = 0; i < kD; ++i) o[i] = fmaf(pj, __bfloat162float(v[(t0 + j) * a.vs + lane * kD + i]), o[i]);
@@ -241,15 +263,15 @@ __device__ __forceinline__ void redo_row(const PrefillArgs& a, const __nv_bfloat
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                    const __grid_constant__ CUtensorMap v_map, const PrefillArgs a, const int n_seqs, const int pair) {
   using Sh = Shape<D>;
   using bf16 = __nv_bfloat16;
-  constexpr int kSlabs = D / 64, kRow = 128, kSlab = 128 * kRow;  // slabs of 64 elements: rows of 128 bytes
+  constexpr int kN = Sh::kN, kSlabs = D / 64, kRow = 128, kSlabQ = kM * kRow, kSlab = kN * kRow;  // slabs of 64 elements: rows of 128 bytes
   constexpr uint32_t kIdS = dec::umma_idesc_bf16(kM, kN, false), kIdO = dec::umma_idesc_bf16(kM, D, true);
   extern __shared__ __align__(1024) uint8_t sm[];
-  Bars& b = *reinterpret_cast<Bars*>(sm + 2 * Sh::kTile + Sh::kStages * Sh::kTile);
+  Bars& b = *reinterpret_cast<Bars*>(sm + 2 * Sh::kQ + Sh::kStages * Sh::kTile);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   // pair: the tiles are heads 2x and 2x + 1; else queries m0 and m0 + 128
   const int columns = pair ? a.heads / 2 : a.heads;
@@ -267,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const int n0 = __shfl_sync(0xffffffffu, steps(0), 0), n1 = __shfl_sync(0xffffffffu, steps(1), 0), n_max = max(n0, n1);
 
-  uint8_t* ring = sm + 2 * Sh::kTile;
+  uint8_t* ring = sm + 2 * Sh::kQ;
   if (tid == 0) {
     dec::mbar_init(&b.q_full, 1);
     for (int i = 0; i < Sh::kStages; ++i) dec::mbar_init(&b.kv_full[i], 1), dec::mbar_init(&b.kv_empty[i], 1);
@@ -281,18 +303,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     dec::fence_mbar_init();
   }
   if (warp == 8) {
-    dec::tmem_alloc(&b.tmem, 512);
+    dec::tmem_alloc(&b.tmem, Sh::kColumns);
     dec::tmem_relinquish();
   }
   dec::tc_fence_before();
   __syncthreads();
   dec::tc_fence_after();
-  // All 512 columns are this block's, so they begin at 0.
-  auto tS = [](int i) { return (uint32_t)(i * kN); };
-  auto tO = [](int i) { return (uint32_t)(2 * kN + i * D); };
+  const uint32_t tm = Sh::kColumns == 512 ? 0 : __shfl_sync(0xffffffffu, b.tmem, 0);  // (all columns begin at 0)
+  auto tS = [&](int i) { return tm + i * kN; };
+  auto tO = [&](int i) { return tm + 2 * kN + i * D; };
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    if (D == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRegsSoftmax));
     // ---- softmax of tile i, one row a thread
     const int i = warp >> 2, row = m0 + i * mstep + (tid & 127), n = i ? n1 : n0, head = head0 + (pair ? i : 0);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
@@ -329,14 +351,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = mn;
         if (j > 0) {
           // S(j) was issued behind P V of the step before: O is at rest until this step's P
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            dec::tmem_ld32(tO(i) + lanes + c * 32, o);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {  // few at a time: the scores are in registers
+            uint32_t o[16];
+            tmem_ld16(tO(i) + lanes + c, o);
             dec::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(tO(i) + lanes + c * 32, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(tO(i) + lanes + c, o);
           }
         }
       }
@@ -345,12 +367,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
       auto weights = [&](auto poly) {
 #pragma unroll
-        for (int c = 0; c < kN / 64; ++c) {
-          uint32_t p[32];
+        for (int c = 0; c < kN / 32; ++c) {
+          uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            F2 y = f2(__uint_as_float(x[2 * c + e / 16][2 * (e % 16)]), __uint_as_float(x[2 * c + e / 16][2 * (e % 16) + 1]));
-            y = fma2(y, sl2, base2);
+          for (int e = 0; e < 16; ++e) {
+            F2 y = fma2(f2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sl2, base2);
             if (e % 8 < decltype(poly)::value) {
               y = exp2_poly(y);
             } else {
@@ -362,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const __nv_bfloat162 h = __floats2bfloat162_rn(u.x, u.y);
             p[e] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          tmem_st32(tS(i) + lanes + c * 32, p);
+          tmem_st16(tS(i) + lanes + c * 16, p);
         }
       };
       if (masked)  // an unseen key's weight is exactly zero
@@ -419,15 +440,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) flag(a.status, DEC_SEQ_TIMEOUT);
     dec::tc_fence_before();
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (D == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kRegsRest));
     if (warp == 9) {
       // ---- loads
       if (n_max > 0 && elect()) {
         const int tiles_q = n1 > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(&b.q_full, tiles_q * Sh::kTile);
+        mbar_arrive_expect_tx(&b.q_full, tiles_q * Sh::kQ);
         for (int i = 0; i < tiles_q; ++i)
           for (int c = 0; c < kSlabs; ++c)
-            tma_load(sm + i * Sh::kTile + c * kSlab, &q_map, c * 64, head0 + (pair ? i : 0), (int)r.q0 + m0 + i * mstep,
+            tma_load(sm + i * Sh::kQ + c * kSlabQ, &q_map, c * 64, head0 + (pair ? i : 0), (int)r.q0 + m0 + i * mstep,
                      &b.q_full);
         int issued = 0;
         auto load = [&](const CUtensorMap* map, int j) {
@@ -464,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect()) {
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-              dec::tc_mma(tS(i), q_desc + ((i * Sh::kTile + (ks / 4) * kSlab + (ks % 4) * 32) >> 4),
+              dec::tc_mma(tS(i), q_desc + ((i * Sh::kQ + (ks / 4) * kSlabQ + (ks % 4) * 32) >> 4),
                           k_desc + kt + (((ks / 4) * kSlab + (ks % 4) * 32) >> 4), kIdS, ks != 0);
             dec::tc_commit(&b.s_full[i]);
           }
@@ -513,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     __syncwarp();
     dec::tc_fence_after();
-    dec::tmem_dealloc(0, 512);
+    dec::tmem_dealloc(tm, Sh::kColumns);
   }
 }
 
@@ -547,19 +568,21 @@ cudaError_t launch(const PrefillArgs& a, int n_seqs, cudaStream_t st) {
   const bool keys = a.n_k > 0;  // without keys every row is zero and no load is issued
   const void *kp = keys ? a.k : a.q, *vp = keys ? a.v : a.q;
   const int rows = keys ? a.n_k : a.n_q, heads = keys ? a.heads / a.gs : a.heads;
-  if (!make_map(&q, a.q, a.n_q, a.heads, D, a.qs, kM) || !make_map(&k, kp, rows, heads, D, keys ? a.ks : a.qs, kN) ||
-      !make_map(&v, vp, rows, heads, D, keys ? a.vs : a.qs, kN))
+  if (!make_map(&q, a.q, a.n_q, a.heads, D, a.qs, kM) || !make_map(&k, kp, rows, heads, D, keys ? a.ks : a.qs, Sh::kN) ||
+      !make_map(&v, vp, rows, heads, D, keys ? a.vs : a.qs, Sh::kN))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
   if (e != cudaSuccess) return e;
-  static const int regs = [] {
-    cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, prefill_kernel<D>) == cudaSuccess ? f.numRegs : 0;
-  }();
-  if (regs != kRegs) return cudaErrorInvalidValue;  // the warps would wait for registers that are not there
+  if (D == 128) {
+    static const int regs = [] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, prefill_kernel<D>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs != Sh::kRegs) return cudaErrorInvalidValue;  // the warps would wait for registers that are not there
+  }
   const int pair = a.gs % 2 == 0, rows_q = pair ? kM : 2 * kM;
   const int64_t blocks = (int64_t)n_seqs * ((a.max_q + rows_q - 1) / rows_q) * (pair ? a.heads / 2 : a.heads);
-  prefill_kernel<D><<<(unsigned)blocks, kThreads, Sh::kSmem, st>>>(q, k, v, a, n_seqs, pair);
+  prefill_kernel<D><<<(unsigned)blocks, Sh::kThreads, Sh::kSmem, st>>>(q, k, v, a, n_seqs, pair);
   return cudaGetLastError();
 }
 
