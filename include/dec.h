@@ -329,7 +329,10 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  * statistics and rotations are fp32 or better; results are rounded once.
  * Limits (DEC_ERR_UNSUPPORTED otherwise): head_dim 64 or 128, n_heads a multiple of
  * n_kv_heads with at most 8 query heads per kv head (query head h reads kv head
- * h / (n_heads / n_kv_heads)).
+ * h / (n_heads / n_kv_heads)); and sizes whose parts are counted in 32 bits:
+ * n_seqs * n_kv_heads * table_stride * page_size / 16 (dec_attention_paged),
+ * n_seqs * n_heads * max_q / 32 (dec_attention_prefill) and n_seqs * 2 * n_kv_heads *
+ * (max_new / page_size + 2) (dec_kv_append) below 2^31.
  *
  * Offsets, lengths and page tables live on the device, so a captured graph can be
  * replayed on other sequences.  A host call cannot refuse what they hold: a
@@ -339,7 +342,8 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
 #define DEC_SEQ_BAD_PAGE 1  /* a page id below 0 or >= n_pages: its positions are left out */
 #define DEC_SEQ_BAD_RANGE 2 /* offsets decreasing, outside the rows given or above the given maximum, or a length
                                that is negative, shorter than its new tokens or longer than its table row: the
-                               sequence is left out (attention: its output rows are zeroed where they are known) */
+                               sequence is left out (attention: its output rows, up to the given maximum, are
+                               zeroed if they can be told) */
 #define DEC_SEQ_TIMEOUT 4   /* a wait inside a kernel ran out (a second; never expected): results are incomplete */
 
 #define DEC_ROPE_HALF 0      /* pairs (j, j + rot_dim/2) */
@@ -373,7 +377,8 @@ typedef struct dec_rope {
 /* Append the new tokens of n_seqs sequences.  Sequence s owns rows cu_new[s] ..
  * cu_new[s + 1] - 1 of q, k and v (none: nothing to do); seq_lens[s] is its length
  * AFTER the append, so its first new token has position seq_lens[s] - (its rows).
- *   - q (nullable) is rotated into q_out (the same buffer and stride: in place);
+ *   - q (nullable) is rotated into q_out, and k, where k_out is given, into k_out (what
+ *     dec_attention_prefill reads); the same buffer and stride: in place;
  *   - k is rotated, k and v are stored.  The scale of a page that starts with this
  *     call is the smallest power of two 2^e, -120 <= e <= 120, with max|x| <= 448 * 2^e
  *     over the page's new finite values; a page that already holds rows of the sequence
@@ -383,13 +388,13 @@ typedef struct dec_rope {
  * Rows behind the last sequence's last row, and page rows that hold no position
  * written here or before, stay as they are.  A page that is written may belong to
  * one sequence of the call only.
- *   q, k, v, q_out  16-byte aligned, row strides multiples of 16 bytes
+ *   q, k, v, q_out, k_out  16-byte aligned, row strides multiples of 16 bytes
  *   max_new         at least the largest number of new tokens of a sequence
  *   n_tokens        rows of q, k and v
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int dec_kv_append(const dec_paged_cache* cache, const dec_rope* rope, int32_t dtype, const void* q, const void* k,
-                  const void* v, void* q_out, int64_t q_stride, int64_t k_stride, int64_t v_stride,
-                  int64_t q_out_stride, int32_t n_heads, int32_t n_seqs, int32_t n_tokens, int32_t max_new,
+                  const void* v, void* q_out, void* k_out, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                  int64_t q_out_stride, int64_t k_out_stride, int32_t n_heads, int32_t n_seqs, int32_t n_tokens, int32_t max_new,
                   const int32_t* cu_new, const int32_t* seq_lens, const int32_t* page_table, int32_t table_stride,
                   int32_t* status, void* stream);
 
@@ -402,7 +407,8 @@ int dec_attention_paged_workspace(const dec_paged_cache* cache, int32_t n_seqs, 
  * empty sequence.  What the pages hold behind the length is never used.
  *   q, out     [n_seqs] rows, 16-byte aligned, strides multiples of 16 bytes
  *   workspace  dec_attention_paged_workspace bytes, 16-byte aligned, nothing to be initialised;
- *              calls that may overlap on the GPU need one each
+ *              calls that may overlap on the GPU need one each, calls in a row (captured or not) can share one
+ * The results do not depend on scheduling: the same inputs give the same bits.
  * Errors: INVALID_ARG (scale not finite and positive, workspace too small, ...), UNSUPPORTED, CUDA. */
 int dec_attention_paged(const dec_paged_cache* cache, int32_t dtype, const void* q, void* out, int64_t q_stride,
                         int64_t out_stride, int32_t n_heads, int32_t n_seqs, const int32_t* seq_lens,

@@ -25,8 +25,8 @@ struct AppendArgs {
   int rot, neighbour;
   float factor;
   const void *q, *k, *v;
-  void* q_out;
-  int64_t qs, ks, vs, qos;
+  void *q_out, *k_out;  // k_out: nullable
+  int64_t qs, ks, vs, qos, kos;
   int heads, n_tokens, max_new, pieces;  // heads: of q (0: no q)
   int kv_blocks, q_blocks;               // of one (sequence, page): they share its kv heads, and its query heads, evenly
   const int32_t *cu, *lens, *table;
@@ -166,12 +166,10 @@ __device__ __forceinline__ void angles(const AppendArgs& a, int c, int64_t pos, 
 // row) where they are few (one token 3.8 us).  A page's scale needs all of its new values, so its keys and values stay in
 // registers between the maximum and the rounding and are read once; the next head's are on their way meanwhile.
 template <typename T, int D, int NIT, int ROLE>
-__global__ void __launch_bounds__(ROLE == kQueries ? 256 : 512, ROLE == kQueries ? 3 : ROLE == kKeysValues && NIT == 1 ? 2 : 1)
-    append_kernel(AppendArgs a) {
+__device__ __forceinline__ void append_block(const AppendArgs& a) {
   __shared__ float red[2][2][16];
   constexpr int kUnits = D / 16;  // threads a row
   constexpr int kBatch = 4;       // query heads whose loads are under way at once
-  asm volatile("griddepcontrol.launch_dependents;");
   const int blocks = (ROLE & kKeysValues ? a.kv_blocks : 0) + (ROLE & kQueries ? a.q_blocks : 0);
   const int part = blockIdx.x % blocks, piece = blockIdx.x / blocks % a.pieces, s = blockIdx.x / blocks / a.pieces;
   const int tid = threadIdx.x, ps = a.c.ps;
@@ -220,7 +218,7 @@ __global__ void __launch_bounds__(ROLE == kQueries ? 256 : 512, ROLE == kQueries
   const bool page_ok = page >= 0 && page < a.c.n_pages;
   if (!page_ok) {
     if (tid == 0) flag(a.status, DEC_SEQ_BAD_PAGE);
-    return;
+    if (!a.k_out) return;
   }
   const int g0 = a.c.hkv * part / a.kv_blocks, g1 = a.c.hkv * (part + 1) / a.kv_blocks;
   float cs[NIT][8], sn[NIT][8];
@@ -253,6 +251,11 @@ __global__ void __launch_bounds__(ROLE == kQueries ? 256 : 512, ROLE == kQueries
         kr[it][0].get(k[it]);
         kr[it][1].get(k[it] + 8);
         if (turned) rotate16(k[it], cs[it], sn[it], neighbour);
+        if (a.k_out) {
+          T* op = static_cast<T*>(a.k_out) + (row0 + row[it]) * a.kos + (int64_t)head * D;
+          Vec8<T>::store(op + d0, k[it]);
+          Vec8<T>::store(op + d1, k[it] + 8);
+        }
         float y[16];
         v[it][0] = vr[it][0];
         v[it][1] = vr[it][1];
@@ -265,6 +268,7 @@ __global__ void __launch_bounds__(ROLE == kQueries ? 256 : 512, ROLE == kQueries
         }
       }
     if (head + 1 < g1) load(head + 1);
+    if (!page_ok) continue;
     const int64_t si = (int64_t)page * a.c.hkv + head;
     float k_was = 0.f, v_was = 0.f;
     if (slot0 > 0) k_was = a.c.ks[si], v_was = a.c.vs[si];
@@ -306,6 +310,15 @@ __global__ void __launch_bounds__(ROLE == kQueries ? 256 : 512, ROLE == kQueries
       }
     __syncthreads();  // red is used again
   }
+}
+
+// Where queries and keys are launches of their own, they run side by side: the second begins once the first's blocks have
+// all begun, and waits for its end at its own end, so that what follows it in the stream follows both.
+template <typename T, int D, int NIT, int ROLE>
+__global__ void __launch_bounds__(ROLE == kQueries ? 256 : 512, ROLE == kQueries ? 3 : ROLE == kKeysValues && NIT == 1 ? 2 : 1)
+    append_kernel(AppendArgs a) {
+  if (ROLE == kQueries) asm volatile("griddepcontrol.launch_dependents;");
+  append_block<T, D, NIT, ROLE>(a);
   if (ROLE == kKeysValues) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
@@ -973,9 +986,9 @@ bool cache_on_device(const dec_paged_cache* c, int dev) {
 }  // namespace
 
 extern "C" int dec_kv_append(const dec_paged_cache* cache, const dec_rope* rope, int32_t dtype, const void* q,
-                             const void* k, const void* v, void* q_out, int64_t q_stride, int64_t k_stride,
-                             int64_t v_stride, int64_t q_out_stride, int32_t n_heads, int32_t n_seqs,
-                             int32_t n_tokens, int32_t max_new, const int32_t* cu_new, const int32_t* seq_lens,
+                             const void* k, const void* v, void* q_out, void* k_out, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int64_t q_out_stride, int64_t k_out_stride,
+                             int32_t n_heads, int32_t n_seqs, int32_t n_tokens, int32_t max_new, const int32_t* cu_new, const int32_t* seq_lens,
                              const int32_t* page_table, int32_t table_stride, int32_t* status, void* stream) {
   int rc = check_cache(cache);
   if (rc) return rc;
@@ -999,20 +1012,22 @@ extern "C" int dec_kv_append(const dec_paged_cache* cache, const dec_rope* rope,
   if (q && (!aligned16(q) || !aligned16(q_out) || !stride_ok(q_stride, (int64_t)n_heads * D, esz) ||
             !stride_ok(q_out_stride, (int64_t)n_heads * D, esz)))
     return DEC_ERR_INVALID_ARG;
+  if (k_out && (!aligned16(k_out) || !stride_ok(k_out_stride, (int64_t)hkv * D, esz))) return DEC_ERR_INVALID_ARG;
+  const int ps = cache->page_size;
+  if (max_new > n_tokens) max_new = n_tokens;  // no valid sequence has more
+  const int64_t pieces = ((int64_t)max_new + ps - 2) / ps + 1, pages = n_seqs * pieces;
+  if (pages * 2 * hkv > INT32_MAX) return DEC_ERR_UNSUPPORTED;
   if (cudaPeekAtLastError() != cudaSuccess) return DEC_ERR_CUDA;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DEC_ERR_CUDA;
   if (!cache_on_device(cache, dev) || !on_device(k, dev) || !on_device(v, dev) || !on_device(cu_new, dev) ||
       !on_device(seq_lens, dev) || !on_device(page_table, dev) || (q && (!on_device(q, dev) || !on_device(q_out, dev))) ||
-      (rope->rot_dim && !on_device(rope->inv_freq, dev)) || (status && !on_device(status, dev)))
+      (k_out && !on_device(k_out, dev)) || (rope->rot_dim && !on_device(rope->inv_freq, dev)) || (status && !on_device(status, dev)))
     return DEC_ERR_INVALID_ARG;
 
-  const int ps = cache->page_size;
-  if (max_new > n_tokens) max_new = n_tokens;  // no valid sequence has more
-  const int64_t pieces = ((int64_t)max_new + ps - 2) / ps + 1, pages = n_seqs * pieces;
   const int units = (max_new < ps ? max_new : ps) * (D / 16);
   AppendArgs a{device_cache(cache), rope->inv_freq, rope->rot_dim, rope->pairs == DEC_ROPE_NEIGHBOUR, rope->factor, q, k,
-               v, q_out, q_stride, k_stride, v_stride, q_out_stride, q ? n_heads : 0, n_tokens, max_new, (int)pieces,
+               v, q_out, k_out, q_stride, k_stride, v_stride, q_out_stride, k_out_stride, q ? n_heads : 0, n_tokens, max_new, (int)pieces,
                hkv, q ? hkv : 0, cu_new, seq_lens, page_table, table_stride, status};
   // A block a kv head, and one for its query heads, is the shortest path for few tokens; more blocks than fill the GPU
   // compute the angles over and over.  With blocks that a page fills (256 threads or more) twice the SMs are enough
@@ -1023,8 +1038,6 @@ extern "C" int dec_kv_append(const dec_paged_cache* cache, const dec_rope* rope,
   const int64_t enough = split ? 2 * 148 : 8 * 148;
   while (a.kv_blocks > 1 && pages * a.kv_blocks > enough) a.kv_blocks = (a.kv_blocks + 1) / 2;
   while (a.q_blocks > 1 && pages * a.q_blocks > enough) a.q_blocks = (a.q_blocks + 1) / 2;
-  const int64_t blocks = pages * (a.kv_blocks + a.q_blocks);
-  if (pages > INT32_MAX || blocks > INT32_MAX) return DEC_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == DEC_BF16)
@@ -1059,6 +1072,8 @@ extern "C" int dec_attention_paged(const dec_paged_cache* cache, int32_t dtype, 
     return DEC_ERR_INVALID_ARG;
   if (n_seqs == 0) return DEC_OK;
   const int hkv = cache->n_kv_heads, D = cache->head_dim, esz = dtype == DEC_BF16 ? 2 : 4;
+  // tiles of 16 positions are counted in 32 bits
+  if ((double)n_seqs * hkv * table_stride * cache->page_size / 16 >= 2147483648.0) return DEC_ERR_UNSUPPORTED;
   if (!q || !out || !seq_lens || !page_table || !workspace || workspace_bytes < need) return DEC_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned4(seq_lens) || !aligned4(page_table) ||
       !aligned4(status) || !stride_ok(q_stride, (int64_t)n_heads * D, esz) ||
@@ -1075,7 +1090,6 @@ extern "C" int dec_attention_paged(const dec_paged_cache* cache, int32_t dtype, 
     return (uint64_t)r() << 32 | r() | 1;
   }();
   const size_t flags = kBlocks * 2 * sizeof(uint64_t);
-  if ((double)n_seqs * hkv * table_stride * cache->page_size / 16 >= 2147483648.0) return DEC_ERR_UNSUPPORTED;
   PagedArgs a{device_cache(cache), q, out, q_stride, out_stride, n_heads / hkv, n_seqs, 31 - __builtin_clz(cache->page_size),
               seq_lens, page_table, table_stride, scale * 1.4426950408889634f,
               reinterpret_cast<float*>(static_cast<char*>(workspace) + flags), static_cast<uint64_t*>(workspace), key, status};

@@ -223,14 +223,14 @@ extern "C" int dec_attention_prefill(int32_t dtype, const void* q, const void* k
       !stride_ok(out_stride, (int64_t)n_heads * D, esz) || !stride_ok(k_stride, (int64_t)n_kv_heads * D, esz) ||
       !stride_ok(v_stride, (int64_t)n_kv_heads * D, esz))
     return DEC_ERR_INVALID_ARG;
+  if (max_q > n_q) max_q = n_q;  // no valid sequence has more
+  if ((int64_t)n_seqs * n_heads * (((int64_t)max_q + 31) / 32) > INT32_MAX) return DEC_ERR_UNSUPPORTED;
   if (cudaPeekAtLastError() != cudaSuccess) return DEC_ERR_CUDA;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DEC_ERR_CUDA;
   if (!on_device(q, dev) || !on_device(out, dev) || !on_device(cu_q, dev) || !on_device(cu_k, dev) ||
       (n_k > 0 && (!on_device(k, dev) || !on_device(v, dev))) || (status && !on_device(status, dev)))
     return DEC_ERR_INVALID_ARG;
-  if (max_q > n_q) max_q = n_q;  // no valid sequence has more
-  if ((int64_t)n_seqs * n_heads * (((int64_t)max_q + 31) / 32) > INT32_MAX) return DEC_ERR_UNSUPPORTED;
   PrefillArgs a{q, k, v, out, q_stride, k_stride, v_stride, out_stride, n_heads, n_heads / n_kv_heads, n_q, n_k, max_q,
                 causal, cu_q, cu_k, scale * 1.4426950408889634f, status};
   cudaStream_t st = static_cast<cudaStream_t>(stream);

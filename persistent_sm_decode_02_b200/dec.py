@@ -118,7 +118,7 @@ def load_library():
             "dec_generate_stop": [P],
             "dec_generate_wait": [P, P, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
             "dec_generate": [P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, ctypes.POINTER(ctypes.c_int32)],
-            "dec_kv_append": [ctypes.POINTER(dec_paged_cache), ctypes.POINTER(dec_rope), I] + [P] * 4 + [LL] * 4
+            "dec_kv_append": [ctypes.POINTER(dec_paged_cache), ctypes.POINTER(dec_rope), I] + [P] * 5 + [LL] * 5
             + [I] * 4 + [P] * 3 + [I, P, P],
             "dec_attention_paged_workspace": [ctypes.POINTER(dec_paged_cache), I, I, ctypes.POINTER(ctypes.c_size_t)],
             "dec_attention_paged": [ctypes.POINTER(dec_paged_cache), I, P, P, LL, LL, I, I, P, P, I, ctypes.c_float,
@@ -229,12 +229,12 @@ def dec_generate(ctx, token_id, n_steps, stop_token, out_tokens, out_count):
     return load_library().dec_generate(ctx, token_id, n_steps, stop_token, out_tokens, out_count)
 
 
-def dec_kv_append(cache, rope, dtype, q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride, n_heads, n_seqs,
-                  n_tokens, max_new, cu_new, seq_lens, page_table, table_stride, status, stream):
+def dec_kv_append(cache, rope, dtype, q, k, v, q_out, k_out, q_stride, k_stride, v_stride, q_out_stride, k_out_stride,
+                  n_heads, n_seqs, n_tokens, max_new, cu_new, seq_lens, page_table, table_stride, status, stream):
     """Rotate and append new tokens to a paged 8-bit cache (device addresses in, status code out); see include/dec.h."""
-    return load_library().dec_kv_append(cache, rope, dtype, q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride,
-                                        n_heads, n_seqs, n_tokens, max_new, cu_new, seq_lens, page_table,
-                                        table_stride, status, stream)
+    return load_library().dec_kv_append(cache, rope, dtype, q, k, v, q_out, k_out, q_stride, k_stride, v_stride,
+                                        q_out_stride, k_out_stride, n_heads, n_seqs, n_tokens, max_new, cu_new,
+                                        seq_lens, page_table, table_stride, status, stream)
 
 
 def dec_attention_paged_workspace(cache, n_seqs, n_heads, out_bytes):
@@ -391,14 +391,17 @@ class PagedCache:
         self.c = dec_paged_cache(k_pages, v_pages, k_scales, v_scales, n_pages, page_size, n_kv_heads, head_dim)
 
     def append(self, q, k, v, q_out, cu_new, seq_lens, page_table, *, table_stride, n_seqs, n_tokens, max_new, n_heads,
-               dtype=DEC_BF16, strides=None, inv_freq=None, rot_dim=0, neighbour_pairs=False, factor=1.0, status=None,
-               stream=None):
-        """dec_kv_append; strides: (q, k, v, q_out).  q and q_out may be None: keys and values alone."""
+               dtype=DEC_BF16, strides=None, inv_freq=None, rot_dim=0, neighbour_pairs=False, factor=1.0, k_out=None,
+               k_out_stride=None, status=None, stream=None):
+        """dec_kv_append; strides: (q, k, v, q_out).  q and q_out may be None: keys and values alone; k_out: where the
+        rotated keys are wanted, too."""
+        kv = self.c.n_kv_heads * self.c.head_dim
         if strides is None:
-            row, kv = n_heads * self.c.head_dim, self.c.n_kv_heads * self.c.head_dim
+            row = n_heads * self.c.head_dim
             strides = (row, kv, kv, row)
         rope = dec_rope(inv_freq, rot_dim, DEC_ROPE_NEIGHBOUR if neighbour_pairs else DEC_ROPE_HALF, factor)
-        _chk_op("dec_kv_append", dec_kv_append(self.c, rope, dtype, q, k, v, q_out, *strides, n_heads, n_seqs, n_tokens,
+        _chk_op("dec_kv_append", dec_kv_append(self.c, rope, dtype, q, k, v, q_out, k_out, *strides,
+                                               kv if k_out_stride is None else k_out_stride, n_heads, n_seqs, n_tokens,
                                                max_new, cu_new, seq_lens, page_table, table_stride, status, stream))
 
     def workspace_bytes(self, n_seqs, n_heads) -> int:

@@ -139,7 +139,7 @@ def rotate64(x, pos, inv_freq, pairs, factor):
 
 
 def run_append(pool, qkv, q_out, h, new, lens, inv_freq, pairs, dtype, factor=1.0, status=None, max_new=None, with_q=True,
-               n_tokens=None):
+               n_tokens=None, k_out=None):
     hkv, d = pool.hkv, pool.d
     x, e, row = qkv.data_ptr(), qkv.element_size(), qkv.stride(0)
     cu = new if isinstance(new, torch.Tensor) else ints(offsets(new))
@@ -150,7 +150,8 @@ def run_append(pool, qkv, q_out, h, new, lens, inv_freq, pairs, dtype, factor=1.
                         max_new=max(new) if max_new is None else max_new, n_heads=h,
                         dtype=DT[dtype][1], strides=(row, row, row, q_out.stride(0)), inv_freq=inv_freq.data_ptr(),
                         rot_dim=2 * inv_freq.numel(), neighbour_pairs=pairs == "neighbour", factor=factor,
-                        status=None if status is None else status.data_ptr(), stream=stream())
+                        k_out=None if k_out is None else k_out.data_ptr(),
+                        k_out_stride=None if k_out is None else k_out.stride(0), status=None if status is None else status.data_ptr(), stream=stream())
     torch.cuda.synchronize()
 
 
@@ -230,8 +231,15 @@ def test_append(case, factor):
     qkv = (torch.randn(sum(new) + 3, (h + 2 * hkv) * d, generator=gen(3), device="cuda") * 1.28).to(DT[dtype][0])
     q_out = torch.full((sum(new) + 3, h, d), 7.0, dtype=DT[dtype][0], device="cuda")
     before = pool.state()
-    run_append(pool, qkv, q_out, h, new, [a + b for a, b in zip(old, new)], freqs(rot), pairs, dtype, factor)
+    k_out = torch.full((sum(new) + 3, hkv, d), 7.0, dtype=qkv.dtype, device="cuda")
+    run_append(pool, qkv, q_out, h, new, [a + b for a, b in zip(old, new)], freqs(rot), pairs, dtype, factor, k_out=k_out)
     check_append(pool, before, qkv, q_out, h, old, new, freqs(rot), pairs, dtype, factor)
+    # the rotated keys, rounded as the queries are
+    pos = torch.cat([torch.arange(a, a + n, device="cuda") for a, n in zip(old, new)])
+    k = rotate64(qkv[:sum(new)].double().view(-1, h + 2 * hkv, d)[:, h:h + hkv], pos, freqs(rot), pairs, factor)
+    err = (k_out[:sum(new)].double() - k).abs()
+    assert bool((err <= DT[dtype][2] * k.abs() + 2.0 ** -19 * qkv.double().abs().amax() * max(1.0, factor)).all())
+    assert bool((k_out[sum(new):] == 7.0).all())
     assert bool((q_out[sum(new):] == 7.0).all())  # rows behind the last sequence
 
 
@@ -284,14 +292,45 @@ def check_append_codes_only(pool, before, x, h, new):
             assert torch.equal(have.nan_to_num(999.0), want.nan_to_num(999.0))
 
 
+def test_append_many_sequences():
+    """400 sequences with 0 to 3 new tokens behind lengths around page ends."""
+    h, hkv, d, ps = 4, 2, 64, 16
+    old, new = [(5 * i) % 35 for i in range(400)], [i % 4 for i in range(400)]
+    lens = [a + b for a, b in zip(old, new)]
+    pool = Pool(lens, hkv, d, ps, 80).fill(old, 81)
+    x = torch.randn(sum(new), (h + 2 * hkv) * d, generator=gen(82), device="cuda")
+    q_out = torch.empty(sum(new), h, d, device="cuda")
+    before = pool.state()
+    run_append(pool, x, q_out, h, new, lens, freqs(d), "half", "f32")
+    check_append(pool, before, x, q_out, h, old, new, freqs(d), "half", "f32")
+
+
+def test_append_whole_prompts_in_full_pages():
+    """Pages that fill a block (queries and keys are launches of their own there), a prompt that starts inside a page."""
+    for dtype, d, ps in (("bf16", 128, 64), ("f32", 128, 128), ("bf16", 64, 128)):
+        h, hkv, old, new = 16, 8, [0, 37, 64], [700, 260, 1]
+        lens = [a + b for a, b in zip(old, new)]
+        pool = Pool(lens, hkv, d, ps, 83).fill(old, 84)
+        x = (torch.randn(sum(new), (h + 2 * hkv) * d, generator=gen(85), device="cuda") * 1.28).to(DT[dtype][0])
+        q_out = torch.empty(sum(new), h, d, dtype=x.dtype, device="cuda")
+        before = pool.state()
+        run_append(pool, x, q_out, h, new, lens, freqs(d), "half", dtype)
+        check_append(pool, before, x, q_out, h, old, new, freqs(d), "half", dtype)
+
+
 def test_append_in_place_and_without_q():
     h, hkv, d, ps, n = 6, 2, 64, 32, 45
     x = (torch.randn(n, (h + 2 * hkv) * d, generator=gen(8), device="cuda")).to(torch.bfloat16)
-    pools = [Pool([n], hkv, d, ps, 9) for _ in range(3)]
+    pools = [Pool([n], hkv, d, ps, 9) for _ in range(5)]
     out = torch.empty(n, h * d, dtype=torch.bfloat16, device="cuda")
     run_append(pools[0], x, out, h, [n], [n], freqs(d), "half", "bf16")
     y = x.clone()
+    z = x.clone()
     run_append(pools[1], y, y, h, [n], [n], freqs(d), "half", "bf16")  # q_out is q, inside the fused buffer
+    k_apart = torch.empty(n, hkv * d, dtype=torch.bfloat16, device="cuda")
+    run_append(pools[3], z, z, h, [n], [n], freqs(d), "half", "bf16", k_out=z[:, h * d:])  # k_out is k, too
+    run_append(pools[4], x, out, h, [n], [n], freqs(d), "half", "bf16", k_out=k_apart)
+    assert torch.equal(z[:, :h * d], out) and torch.equal(z[:, h * d:(h + hkv) * d], k_apart)
     run_append(pools[2], x, out, h, [n], [n], freqs(d), "half", "bf16", with_q=False)
     assert torch.equal(y[:, :h * d], out) and torch.equal(y[:, h * d:], x[:, h * d:])
     for p in pools[1:]:
@@ -351,10 +390,12 @@ def test_append_inconsistent_sequences_are_skipped(what):
         max_new, keep = 9, [1, 2]
     before = pool.state()
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    run_append(pool, x, q_out, h, ints(cu), lens, freqs(d), "half", "f32", status=status, max_new=max_new)
+    k_out = torch.full((sum(new), hkv, d), 7.0, device="cuda")
+    run_append(pool, x, q_out, h, ints(cu), lens, freqs(d), "half", "f32", status=status, max_new=max_new, k_out=k_out)
     assert int(status) == bits
     pool.table = table
-    if what == "page":  # slots 0..15 of sequence 1 are left out, 16..18 and every rotated query are there
+    if what == "page":  # slots 0..15 of sequence 1 are left out, 16..18 and every rotated query and key are there
+        assert not bool((k_out == 7.0).all(-1).any())
         assert not bool((q_out == 7.0).all(-1).any())
         first = int(table[1, 0])
         assert torch.equal(pool.k[first], before[0][first])
@@ -403,6 +444,11 @@ PAGED = [
     (3, 3, 64, 32, list(range(70))),
     (2, 2, 128, 128, [20000]),
     (1, 1, 64, 16, [0]),
+    (4, 1, 64, 16, [17] * 32),                                    # as many sequences as one warp counts
+    (4, 1, 64, 16, [17] * 16 + [0] + [300] + [16] * 15),          # one more
+    (2, 1, 128, 16, [(7 * i) % 41 for i in range(1000)]),         # several for a thread, empty ones among them
+    (1, 1, 64, 32, [3] * 2500),                                   # more than there are warps
+    (8, 8, 128, 16, [1, 2000, 1, 1, 700, 0, 33]),                 # one query head a kv head; long between short
 ]
 
 
@@ -424,6 +470,56 @@ def test_paged(case, dtype):
     again = torch.empty_like(out[:-1])
     run_paged(pool, q, again, lens, dtype)
     assert torch.equal(again, out[:-1])  # the same bits every time
+
+
+def test_paged_everything_empty():
+    pool = Pool([0, 0, 0], 2, 64, 16, 18)
+    q = torch.randn(3, 4, 64, generator=gen(19), device="cuda")
+    out = torch.full_like(q, 7.0)
+    run_paged(pool, q, out, [0, 0, 0], "f32")
+    assert bool((out == 0).all())
+
+
+def test_paged_scales_far_apart():
+    """V's scales of one head span 2^40 between pages (a page of zeros has the smallest there is): the small ones' share
+    of the result is kept where the large ones' weights vanish."""
+    h, hkv, d, ps, lens = 4, 2, 64, 16, [96]
+    pool = Pool(lens, hkv, d, ps, 16).fill(lens, 17)
+    for p, e in enumerate((-120, -30, -6, 10, -20, -7)):
+        page = int(pool.table[0, p])
+        pool.vs[page] = 2.0 ** e
+        if e == -120:
+            pool.v[page] = 0
+    q = torch.randn(1, h, d, generator=gen(15), device="cuda")
+    k, _ = pool.rows(0, 96)
+    for g in range(hkv):  # queries that avoid the page with the large values: scores around -64 there
+        q[0, 2 * g:2 * g + 2] = -200.0 * k[g, 48:64].mean(0).float() / k[g, 48:64].mean(0).norm().float()
+    for dtype in ("f32", "bf16"):
+        x = q.to(DT[dtype][0])
+        out = torch.empty_like(x)
+        run_paged(pool, x, out, lens, dtype)
+        check_paged(pool, x, out, lens, dtype)
+
+
+def test_paged_two_streams_at_once():
+    """Calls under way together, each with a workspace of its own."""
+    h, hkv, d, ps = 8, 2, 128, 32
+    sets = [[4000, 10, 900], [50] * 40, [20000]]
+    pools = [Pool(lens, hkv, d, ps, 90 + i).fill(lens, 93 + i) for i, lens in enumerate(sets)]
+    q = [torch.randn(len(l), h, d, generator=gen(96), device="cuda") for l in sets]
+    out = [torch.empty_like(x) for x in q]
+    space = [torch.full((p.cache().workspace_bytes(len(l), h),), 0x5A, dtype=torch.uint8, device="cuda")
+             for p, l in zip(pools, sets)]
+    lens = [ints(l) for l in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                run_paged(pools[i], q[i], out[i], lens[i], "f32", space=space[i])
+    torch.cuda.synchronize()
+    for i, l in enumerate(sets):
+        check_paged(pools[i], q[i], out[i], l, "f32")
 
 
 def test_paged_scales_and_large_scores():
@@ -565,6 +661,10 @@ PREFILL = [
     (7, 1, 64, [300, 10], [20, 4]),          # queries before the first key see nothing
     (2, 2, 128, [3, 2], [0, 5]),
     (8, 2, 64, [1700], None),
+    (4, 2, 64, [1, 0, 3, 5, 2] * 60, None),  # many tiny prompts
+    (3, 1, 64, [200, 70], None),             # three heads of one kv head: none to pair with
+    (6, 2, 128, [140, 300], None),           # the same, heads of 128
+    (2, 2, 64, [4, 2], [0, 0]),              # no keys at all
 ]
 
 
@@ -707,12 +807,11 @@ def chain(dtype, h, hkv, d, ps, prompts, steps, capture):
     with torch.cuda.stream(work):
         st = work.cuda_stream
         cu, lens = ints(offsets(prompts)), ints(prompts)
+        kr = torch.empty(sum(prompts), hkv, d, dtype=t, device="cuda")
         c.append(x.data_ptr(), x.data_ptr() + h * d * e, x.data_ptr() + (h + hkv) * d * e, q0.data_ptr(), cu.data_ptr(),
                  lens.data_ptr(), pool.table.data_ptr(), table_stride=pool.width, n_seqs=n, n_tokens=sum(prompts),
                  max_new=max(prompts), n_heads=h, dtype=DT[dtype][1], strides=(row, row, row, h * d),
-                 inv_freq=fr.data_ptr(), rot_dim=d, stream=st)
-        kr = rotate64(x.double().view(-1, h + 2 * hkv, d)[:, h:h + hkv],
-                      torch.cat([torch.arange(p, device="cuda") for p in prompts]), fr, "half", 1.0).to(t).contiguous()
+                 inv_freq=fr.data_ptr(), rot_dim=d, k_out=kr.data_ptr(), stream=st)
         o0 = torch.empty_like(q0)
         v = x.view(-1, h + 2 * hkv, d)[:, h + hkv:]
         pkg.attention_prefill(q0.data_ptr(), kr.data_ptr(), v.data_ptr(), o0.data_ptr(), cu.data_ptr(), cu.data_ptr(),

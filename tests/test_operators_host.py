@@ -24,8 +24,8 @@ def cache(**over):
 
 
 def append(c=None, rope=None, **over):
-    a = dict(dtype=D_.DEC_BF16, q=P, k=P, v=P, q_out=P, q_stride=256, k_stride=128, v_stride=128, q_out_stride=256,
-             n_heads=4, n_seqs=1, n_tokens=3, max_new=3, cu_new=P, seq_lens=P, page_table=P, table_stride=2, status=None,
+    a = dict(dtype=D_.DEC_BF16, q=P, k=P, v=P, q_out=P, k_out=None, q_stride=256, k_stride=128, v_stride=128,
+             q_out_stride=256, k_out_stride=128, n_heads=4, n_seqs=1, n_tokens=3, max_new=3, cu_new=P, seq_lens=P, page_table=P, table_stride=2, status=None,
              stream=None)
     a.update(over)
     return D_.dec_kv_append(cache() if c is None else c, D_.dec_rope(P, 64, 0, 1.0) if rope is None else rope, *a.values())
@@ -74,7 +74,8 @@ def test_cache_is_checked(over, rc):
 
 @pytest.mark.parametrize("over", [dict(dtype=D_.DEC_FP8_E4M3_B128), dict(dtype=9), dict(k=None), dict(v=None), dict(q=None),
                                   dict(q_out=None), dict(cu_new=None), dict(seq_lens=None), dict(page_table=None),
-                                  dict(q=P + 2), dict(k=P + 8), dict(v=P + 4), dict(q_out=P + 8), dict(cu_new=P + 1),
+                                  dict(q=P + 2), dict(k=P + 8), dict(v=P + 4), dict(k_out=P + 8),
+                                  dict(k_out=P, k_out_stride=120), dict(q_out=P + 8), dict(cu_new=P + 1),
                                   dict(status=P + 2), dict(q_stride=248), dict(q_stride=257), dict(k_stride=127),
                                   dict(v_stride=132), dict(q_out_stride=0), dict(n_seqs=-1), dict(n_tokens=-1),
                                   dict(max_new=-1), dict(table_stride=-1)], ids=str)
@@ -115,6 +116,12 @@ def test_attention_is_checked(over):
                                      (dict(scale=float("inf")), INVALID)], ids=str)
 def test_prefill_is_checked(over, rc):
     assert prefill(**over) == rc
+
+
+def test_sizes_past_what_is_counted_in_32_bits_are_refused():
+    assert attention(n_seqs=1 << 16, table_stride=1 << 16) == UNSUPPORTED  # 2^16 * 2 * 2^16 tiles of 16
+    assert prefill(n_seqs=1 << 30, n_q=1 << 30, max_q=1 << 20) == UNSUPPORTED
+    assert append(n_seqs=1 << 30, n_tokens=1 << 30, max_new=1 << 20) == UNSUPPORTED
 
 
 def test_nothing_to_do_is_no_error():
