@@ -7,7 +7,7 @@ ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", "dec_api.cu"), os.path.join(HERE, "csrc", "noalloc.cu"),
            os.path.join(HERE, "csrc", "paged.cu"), os.path.join(HERE, "csrc", "prefill.cu")]
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-Xcompiler", "-fPIC",
-         "-shared", "-I", os.path.join(ROOT, "include")]
+         "-shared", "--threads", "0", "-I", os.path.join(ROOT, "include")]
 
 
 def build(verbose: bool = False) -> str:

@@ -3,7 +3,7 @@
 // A block takes two tiles of 128 queries that read the same keys (two heads of one kv head, or neighbouring queries
 // of one head), and walks their keys in steps of kN:
 //   S = Q K^T (128 x kN, fp32 in TMEM), P = 2^(scale log2(e) S - m) rounded to bf16 over S, O += P V.
-// Warps 0-3 and 4-7 are the tiles' softmax, a thread a row; warp 8 issues every MMA; warp 9 every TMA load.
+// Warps 0-3 and 4-7 are the tiles' softmax, a thread a row; warp 8 issues every MMA; warp 9 every TMA load; warp 10 finds work.
 //   TMEM: S0 | S1 (kN columns each, P in the first kN / 2) | O0 | O1 (D columns each)
 //   shared memory: Q, and a ring of K and V tiles, rows of 128 bytes in the 128-byte swizzle
 // The tiles alternate: while one tile's softmax runs, the tensor cores do the other's P V and next Q K^T.
@@ -22,8 +22,7 @@
 // rate); of heads of 64 325 us.  With the softmax left out the MMAs, loads and hand-overs take 395 us: the tensor cores wait
 // for hand-overs (about 800 cycles from S to P and on, two tiles to hide them) and for shared memory (Q K^T reads both
 // operands there at its full 128 bytes a cycle).  Tried and slower: two threads a row (115 against 100 us for six ragged
-// prompts of up to 1500, heads of 64; spills at 128), steps of 64 keys with two S buffers for heads of 128 (543), blocks that
-// stay for several pairs of tiles by a fixed plan (544: the plan's imbalance, and registers).
+// prompts of up to 1500, heads of 64; spills at 128), steps of 64 keys with two S buffers for heads of 128 (543).
 #pragma once
 #include <cuda.h>
 
@@ -74,28 +73,39 @@ constexpr int kPoly = 2;
 constexpr float kC0 = 0x1.fff692p-1f, kC1 = 0x1.62f31ap-1f, kC2 = 0x1.f0de1ap-3f, kC3 = 0x1.c3f75ep-5f;
 
 // Heads of 128: S and O of two tiles with steps of 128 keys fill an SM's TMEM, one block has the SM to itself, and its
-// softmax threads keep a row of S in registers that they take over from the last warpgroup.
+// softmax threads keep a row of S in registers that they take over from the last warpgroup.  The block stays: warp 10 asks
+// for the work of blocks that have not begun, and while the softmax warps write one pair of tiles the next one's loads and
+// Q K^T are under way (16 ragged prompts of up to 512: 52 us, a block for each pair 64; one of 8192: 440 / 448).
 // Heads of 64: with steps of 64 keys they fill half of it, and two blocks share an SM (shared memory lets no third in):
 // four tiles whose waits overlap, as do one block's first loads and last stores with the other's steps.
 template <int D>
 struct Shape {
   static constexpr int kN = D;                // keys of a step
   static constexpr int kBlocks = 128 / D;     // on an SM
+  static constexpr bool kStay = D == 128;     // a block takes work until there is none
   static constexpr int kColumns = 4 * D;      // of TMEM
   static constexpr int kThreads = D == 128 ? 384 : 320;
   static constexpr int kRegs = 168, kRegsSoftmax = 208, kRegsRest = 88;  // heads of 128: at launch, and handed over
   static_assert(D != 128 || 256 * kRegsSoftmax + 128 * kRegsRest <= kThreads * kRegs, "those at launch");
   static constexpr int kQ = kM * D * 2, kTile = kN * D * 2;  // bytes of a query tile, of a step's keys or values
   static constexpr int kStages = D == 128 ? 4 : 8;
-  static constexpr int kSmem = 2 * kQ + kStages * kTile + 512;  // barriers behind the tiles
+  static constexpr int kSmem = 2 * kQ + kStages * kTile + 512;  // Bars behind the tiles
   static_assert(kSmem <= 227 * 1024 / kBlocks - 1024 && kSmem > 227 * 1024 / (kBlocks + 1), "blocks on an SM");
 };
 
-struct Bars {
-  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], drained;
+// What a block works on: two tiles of queries and the keys they see.
+struct Item {
+  int q0, k0, lq, lk, m0, head0, n[2], sound;  // n: steps of each tile; sound: the sequence's ranges are
+};
+
+struct Bars {  // at most 512 bytes
+  uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2], next, drained;
+  Item item[2];
+  uint4 answer;  // of the request for more work
   uint32_t tmem;
   int dead;
 };
+constexpr int kTakers = 10;  // warps that read an item
 
 // One lane of a converged warp.  What an MMA is issued with must be the same for the warp in the compiler's eyes too: the
 // issuing warp's loops run in all lanes, over values from shuffles and votes.  Under `lane == 0`, or with loop bounds
@@ -130,6 +140,27 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* d
   for (int i = 0; i < 16; ++i)
     if (__all_sync(0xffffffffu, dec::mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_slow(bar, parity, dead));
+}
+
+// More work: the number of a block of this launch that has not begun and now never will, in place of which this block
+// does its work; none left: -1.  The answer arrives in shared memory.
+__device__ __forceinline__ void ask(uint4* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ int answer_of(const uint4* answer) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok ? (int)x : -1;
 }
 
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int head, int row, uint64_t* bar) {
@@ -265,7 +296,8 @@ __device__ __forceinline__ void redo_row(const PrefillArgs& a, const __nv_bfloat
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                   const __grid_constant__ CUtensorMap v_map, const PrefillArgs a, const int n_seqs, const int pair) {
+                   const __grid_constant__ CUtensorMap v_map, const PrefillArgs a, const int n_seqs, const int items,
+                   const int pair) {
   using Sh = Shape<D>;
   using bf16 = __nv_bfloat16;
   constexpr int kN = Sh::kN, kSlabs = D / 64, kRow = 128, kSlabQ = kM * kRow, kSlab = kN * kRow;  // slabs of 64 elements: rows of 128 bytes
@@ -273,31 +305,40 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
   extern __shared__ __align__(1024) uint8_t sm[];
   Bars& b = *reinterpret_cast<Bars*>(sm + 2 * Sh::kQ + Sh::kStages * Sh::kTile);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  // pair: the tiles are heads 2x and 2x + 1; else queries m0 and m0 + 128
-  const int columns = pair ? a.heads / 2 : a.heads;
-  const int head0 = (pair ? 2 : 1) * (blockIdx.x % columns), s = blockIdx.x / columns % n_seqs;
-  const int tile = gridDim.x / columns / n_seqs - 1 - blockIdx.x / columns / n_seqs;  // long rows first
-  const Range r = range_of(a, s);
-  if (!r.ok && tid == 0) flag(a.status, DEC_SEQ_BAD_RANGE);
-  const int m0 = tile * (pair ? kM : 2 * kM), mstep = pair ? 0 : kM, kvh = head0 / a.gs, shift = r.lk - r.lq;
-  if (m0 >= r.lq) return;
-  // steps of a tile, up to the last key its last row sees
-  auto steps = [&](int i) {
-    const int mi = m0 + i * mstep;
-    const int keys = !r.ok || mi >= r.lq ? 0 : a.causal ? min(r.lk, min(mi + kM, r.lq) + shift) : r.lk;
-    return keys > 0 ? (keys + kN - 1) / kN : 0;
+  const int columns = pair ? a.heads / 2 : a.heads, mstep = pair ? 0 : kM;
+  // Work `at` of the launch.  pair: the tiles are heads 2x and 2x + 1; else queries m0 and m0 + 128.  Late queries, with
+  // most keys, first.  false: the sequence ends before it.
+  auto item_at = [&](int at, Item& w) {
+    const int s = at / columns % n_seqs;
+    const Range r = range_of(a, s);
+    w.q0 = (int)r.q0, w.k0 = (int)r.k0, w.lq = r.lq, w.lk = r.lk, w.sound = r.ok;
+    w.head0 = (pair ? 2 : 1) * (at % columns);
+    w.m0 = (items / columns / n_seqs - 1 - at / columns / n_seqs) * (pair ? kM : 2 * kM);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // steps of a tile, up to the last key its last row sees
+      const int mi = w.m0 + i * mstep;
+      const int keys = !r.ok || mi >= r.lq ? 0 : a.causal ? min(r.lk, min(mi + kM, r.lq) + r.lk - r.lq) : r.lk;
+      w.n[i] = keys > 0 ? (keys + kN - 1) / kN : 0;
+    }
+    if (!r.ok && lane == 0) flag(a.status, DEC_SEQ_BAD_RANGE);
+    return w.m0 < r.lq;
   };
-  const int n0 = __shfl_sync(0xffffffffu, steps(0), 0), n1 = __shfl_sync(0xffffffffu, steps(1), 0), n_max = max(n0, n1);
+  Item only;  // where a block has one
+  if (!Sh::kStay && !item_at(blockIdx.x, only)) return;
 
   uint8_t* ring = sm + 2 * Sh::kQ;
   if (tid == 0) {
     dec::mbar_init(&b.q_full, 1);
+    dec::mbar_init(&b.q_empty, 1);
     for (int i = 0; i < Sh::kStages; ++i) dec::mbar_init(&b.kv_full[i], 1), dec::mbar_init(&b.kv_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       dec::mbar_init(&b.s_full[i], 1);
       dec::mbar_init(&b.p_full[i], kM);
       dec::mbar_init(&b.o_full[i], 1);
+      dec::mbar_init(&b.item_full[i], 1);
+      dec::mbar_init(&b.item_empty[i], kTakers);
     }
+    dec::mbar_init(&b.next, 1);
     dec::mbar_init(&b.drained, 1);
     b.dead = 0;
     dec::fence_mbar_init();
@@ -312,175 +353,229 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
   const uint32_t tm = Sh::kColumns == 512 ? 0 : __shfl_sync(0xffffffffu, b.tmem, 0);  // (all columns begin at 0)
   auto tS = [&](int i) { return tm + i * kN; };
   auto tO = [&](int i) { return tm + 2 * kN + i * D; };
+  bool ok = true;
+  // The round-th item; the caller's warp has done with it at leave().  false: there is none.
+  auto take = [&](uint32_t round, Item& w) {
+    if (!Sh::kStay) {
+      w = only;
+      return round == 0;
+    }
+    ok = ok && wait_warp(&b.item_full[round & 1], round >> 1 & 1, &b.dead);
+    if (!ok) return false;
+    w = b.item[round & 1];
+    return w.m0 >= 0;
+  };
+  auto leave = [&](uint32_t round) {
+    __syncwarp();
+    if (Sh::kStay && lane == 0) mbar_arrive(&b.item_empty[round & 1]);
+  };
 
   if (warp < 8) {
-    if (D == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRegsSoftmax));
+    if (Sh::kStay) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::kRegsSoftmax));
     // ---- softmax of tile i, one row a thread
-    const int i = warp >> 2, row = m0 + i * mstep + (tid & 127), n = i ? n1 : n0, head = head0 + (pair ? i : 0);
+    const int i = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
-    const int end = !r.ok ? 0 : a.causal ? min(r.lk, row + shift + 1) : r.lk;  // keys the row sees
-    const int warp_end = __shfl_sync(0xffffffffu, end, 0);  // the fewest in the warp
     const float sl = a.scale_log2;
-    float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      ok = __all_sync(0xffffffffu, wait(&b.s_full[i], j & 1, &b.dead));
-      if (!ok) break;
-      dec::tc_fence_after();
-      uint32_t x[kN / 32][32];
-#pragma unroll
-      for (int c = 0; c < kN / 32; ++c) dec::tmem_ld32(tS(i) + lanes + c * 32, x[c]);
-      dec::tmem_wait_ld();
-      const bool masked = j * kN + kN > warp_end;
-      if (masked) {
-        const int lim = end - j * kN;
-#pragma unroll
-        for (int e = 0; e < kN; ++e)
-          if (e >= lim) x[e / 32][e % 32] = 0xFF800000u;
+    uint32_t step = 0, written = 0;  // of all items: the barriers' phases
+    for (uint32_t round = 0;; ++round) {
+      int n, end, warp_end;  // steps, keys the row sees, and the fewest in the warp
+      {
+        Item w;
+        if (!take(round, w)) break;
+        n = i ? w.n[1] : w.n[0];
+        end = !w.sound ? 0 : a.causal ? min(w.lk, w.m0 + i * mstep + (tid & 127) + w.lk - w.lq + 1) : w.lk;
+        warp_end = __shfl_sync(0xffffffffu, end, 0);
       }
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++step) {
+        ok = wait_warp(&b.s_full[i], step & 1, &b.dead);
+        if (!ok) break;
+        dec::tc_fence_after();
+        uint32_t x[kN / 32][32];
 #pragma unroll
-      for (int e = 0; e < kN; e += 2)
-        mx4[e / 2 % 4] = fmaxf(mx4[e / 2 % 4], fmaxf(__uint_as_float(x[e / 32][e % 32]), __uint_as_float(x[e / 32][e % 32 + 1])));
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-      const bool grow = (mx - m) * sl > 8.f || (m == -INFINITY && mx > m);
-      if (__any_sync(0xffffffffu, grow)) {
-        const float mn = grow ? mx : m;
-        const float f = grow ? dec::ex2_approx((m - mn) * sl) : 1.f;
-        l *= f;
-        m = mn;
-        if (j > 0) {
-          // S(j) was issued behind P V of the step before: O is at rest until this step's P
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {  // few at a time: the scores are in registers
-            uint32_t o[16];
-            tmem_ld16(tO(i) + lanes + c, o);
-            dec::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st16(tO(i) + lanes + c, o);
-          }
-        }
-      }
-      const float base = m == -INFINITY ? 0.f : m * sl;
-      const F2 sl2 = f2(sl, sl), base2 = f2(-base, -base);
-      F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-      auto weights = [&](auto poly) {
-#pragma unroll
-        for (int c = 0; c < kN / 32; ++c) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            F2 y = fma2(f2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sl2, base2);
-            if (e % 8 < decltype(poly)::value) {
-              y = exp2_poly(y);
-            } else {
-              const float2 u = un2(y);
-              y = f2(dec::ex2_approx(u.x), dec::ex2_approx(u.y));
-            }
-            sum[e & 1] = add2(sum[e & 1], y);
-            const float2 u = un2(y);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(u.x, u.y);
-            p[e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          tmem_st16(tS(i) + lanes + c * 16, p);
-        }
-      };
-      if (masked)  // an unseen key's weight is exactly zero
-        weights(std::integral_constant<int, 0>());
-      else
-        weights(std::integral_constant<int, kPoly>());
-      const float2 sums = un2(add2(sum[0], sum[1]));
-      l += sums.x + sums.y;
-      tmem_wait_st();
-      dec::tc_fence_before();
-      mbar_arrive(&b.p_full[i]);
-    }
-    // ---- results
-    if (ok && n > 0) {
-      ok = __all_sync(0xffffffffu, wait(&b.o_full[i], 0, &b.dead));
-      dec::tc_fence_after();
-    }
-    const bool live = row < r.lq;
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    bf16* op = static_cast<bf16*>(a.out) + (r.q0 + row) * a.os + (int64_t)head * D;
-    bool bad = false;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t o[32];
-      if (ok && n > 0) {
-        dec::tmem_ld32(tO(i) + lanes + c * 32, o);
+        for (int c = 0; c < kN / 32; ++c) dec::tmem_ld32(tS(i) + lanes + c * 32, x[c]);
         dec::tmem_wait_ld();
-      } else {
+        const bool masked = j * kN + kN > warp_end;
+        if (masked) {
+          const int lim = end - j * kN;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0;
-      }
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        float y[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          y[k] = l != 0.f ? __uint_as_float(o[e + k]) * inv : 0.f;
-          bad |= !(fabsf(y[k]) <= 3.38953139e38f);  // bf16's largest: not finite, or rounding to infinity
+          for (int e = 0; e < kN; ++e)
+            if (e >= lim) x[e / 32][e % 32] = 0xFF800000u;
         }
-        if (live) Vec8<bf16>::store(op + c * 32 + e, y);
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < kN; e += 2)
+          mx4[e / 2 % 4] =
+              fmaxf(mx4[e / 2 % 4], fmaxf(__uint_as_float(x[e / 32][e % 32]), __uint_as_float(x[e / 32][e % 32 + 1])));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        const bool grow = (mx - m) * sl > 8.f || (m == -INFINITY && mx > m);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? mx : m;
+          const float f = grow ? dec::ex2_approx((m - mn) * sl) : 1.f;
+          l *= f;
+          m = mn;
+          if (j > 0) {
+            // S(j) was issued behind P V of the step before: O is at rest until this step's P
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {  // few at a time: the scores are in registers
+              uint32_t o[16];
+              tmem_ld16(tO(i) + lanes + c, o);
+              dec::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(tO(i) + lanes + c, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m * sl;
+        const F2 sl2 = f2(sl, sl), base2 = f2(-base, -base);
+        F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+        auto weights = [&](auto poly) {
+#pragma unroll
+          for (int c = 0; c < kN / 32; ++c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              F2 y = fma2(f2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sl2, base2);
+              if (e % 8 < decltype(poly)::value) {
+                y = exp2_poly(y);
+              } else {
+                const float2 u = un2(y);
+                y = f2(dec::ex2_approx(u.x), dec::ex2_approx(u.y));
+              }
+              sum[e & 1] = add2(sum[e & 1], y);
+              const float2 u = un2(y);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(u.x, u.y);
+              p[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            tmem_st16(tS(i) + lanes + c * 16, p);
+          }
+        };
+        if (masked)  // an unseen key's weight is exactly zero
+          weights(std::integral_constant<int, 0>());
+        else
+          weights(std::integral_constant<int, kPoly>());
+        const float2 sums = un2(add2(sum[0], sum[1]));
+        l += sums.x + sums.y;
+        tmem_wait_st();
+        dec::tc_fence_before();
+        mbar_arrive(&b.p_full[i]);
       }
-    }
-    uint32_t again = __ballot_sync(0xffffffffu, bad && live && end > 0 && ok);
-    while (again) {
-      const int w = __ffs(again) - 1;
-      again &= again - 1;
-      const int64_t rw = __shfl_sync(0xffffffffu, row, w);
-      __syncwarp();  // the row's first result is written
-      redo_row<D>(a, static_cast<const bf16*>(a.q) + (r.q0 + rw) * a.qs + (int64_t)head * D,
-                  static_cast<const bf16*>(a.k) + r.k0 * a.ks + (int64_t)kvh * D,
-                  static_cast<const bf16*>(a.v) + r.k0 * a.vs + (int64_t)kvh * D,
-                  static_cast<bf16*>(a.out) + (r.q0 + rw) * a.os + (int64_t)head * D, __shfl_sync(0xffffffffu, end, w));
+      if (!ok) break;
+      // ---- results
+      if (n > 0) {
+        ok = wait_warp(&b.o_full[i], written++ & 1, &b.dead);
+        if (!ok) break;
+        dec::tc_fence_after();
+      }
+      Item w;  // read again: the loop above needs the registers
+      if (Sh::kStay) w = b.item[round & 1]; else w = only;
+      leave(round);
+      const int row = w.m0 + i * mstep + (tid & 127), head = w.head0 + (pair ? i : 0);
+      const bool live = row < w.lq;
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      bf16* op = static_cast<bf16*>(a.out) + ((int64_t)w.q0 + row) * a.os + (int64_t)head * D;
+      bool bad = false;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          dec::tmem_ld32(tO(i) + lanes + c * 32, o);
+          dec::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            y[k] = l != 0.f ? __uint_as_float(o[e + k]) * inv : 0.f;
+            bad |= !(fabsf(y[k]) <= 3.38953139e38f);  // bf16's largest: not finite, or rounding to infinity
+          }
+          if (live) Vec8<bf16>::store(op + c * 32 + e, y);
+        }
+      }
+      dec::tc_fence_before();  // O is read: the next item's first P lets it be written
+      uint32_t again = __ballot_sync(0xffffffffu, bad && live && end > 0);
+      while (again) {
+        const int k = __ffs(again) - 1;
+        again &= again - 1;
+        const int64_t rw = __shfl_sync(0xffffffffu, row, k);
+        __syncwarp();  // the row's first result is written
+        redo_row<D>(a, static_cast<const bf16*>(a.q) + (w.q0 + rw) * a.qs + (int64_t)head * D,
+                    static_cast<const bf16*>(a.k) + (int64_t)w.k0 * a.ks + (int64_t)(head / a.gs) * D,
+                    static_cast<const bf16*>(a.v) + (int64_t)w.k0 * a.vs + (int64_t)(head / a.gs) * D,
+                    static_cast<bf16*>(a.out) + (w.q0 + rw) * a.os + (int64_t)head * D,
+                    __shfl_sync(0xffffffffu, end, k));
+      }
     }
     if (!ok && lane == 0) flag(a.status, DEC_SEQ_TIMEOUT);
     dec::tc_fence_before();
   } else {
-    if (D == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kRegsRest));
+    if (Sh::kStay) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::kRegsRest));
     if (warp == 9) {
-      // ---- loads
-      if (n_max > 0 && elect()) {
-        const int tiles_q = n1 > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(&b.q_full, tiles_q * Sh::kQ);
-        for (int i = 0; i < tiles_q; ++i)
-          for (int c = 0; c < kSlabs; ++c)
-            tma_load(sm + i * Sh::kQ + c * kSlabQ, &q_map, c * 64, head0 + (pair ? i : 0), (int)r.q0 + m0 + i * mstep,
-                     &b.q_full);
-        int issued = 0;
-        auto load = [&](const CUtensorMap* map, int j) {
-          const int slot = issued % Sh::kStages, round = issued / Sh::kStages;
-          if (round > 0 && !wait(&b.kv_empty[slot], (round - 1) & 1, &b.dead)) return false;
-          mbar_arrive_expect_tx(&b.kv_full[slot], Sh::kTile);
-          for (int c = 0; c < kSlabs; ++c)
-            tma_load(ring + slot * Sh::kTile + c * kSlab, map, c * 64, kvh, (int)r.k0 + j * kN, &b.kv_full[slot]);
-          ++issued;
-          return true;
-        };
-        bool ok = true;
-        for (int j = 0; j < n_max && ok; ++j) ok = load(&k_map, j) && load(&v_map, j);
-        if (b.dead) {  // no copy may be in flight when the block ends
-          wait_slow(&b.q_full, 0, nullptr);
-          for (int x = max(0, issued - Sh::kStages); x < issued; ++x)
-            wait_slow(&b.kv_full[x % Sh::kStages], (x / Sh::kStages) & 1, nullptr);
+      // ---- loads: an item's Q, then its K0 V0 K1 V1 ... round the ring
+      int issued = 0, n_q = 0;
+      for (uint32_t round = 0;; ++round) {
+        Item w;
+        if (!take(round, w)) break;
+        leave(round);
+        const int n_max = max(w.n[0], w.n[1]);
+        if (n_max > 0 && elect()) {
+          ok = n_q == 0 || wait(&b.q_empty, (n_q - 1) & 1, &b.dead);
+          if (ok) {
+            const int tiles_q = w.n[1] > 0 ? 2 : 1;
+            mbar_arrive_expect_tx(&b.q_full, tiles_q * Sh::kQ);
+            for (int i = 0; i < tiles_q; ++i)
+              for (int c = 0; c < kSlabs; ++c)
+                tma_load(sm + i * Sh::kQ + c * kSlabQ, &q_map, c * 64, w.head0 + (pair ? i : 0), w.q0 + w.m0 + i * mstep,
+                         &b.q_full);
+            ++n_q;
+          }
+          for (int j = 0; j < 2 * n_max && ok; ++j) {
+            const int slot = issued % Sh::kStages, turn = issued / Sh::kStages;
+            ok = turn == 0 || wait(&b.kv_empty[slot], (turn - 1) & 1, &b.dead);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&b.kv_full[slot], Sh::kTile);
+            for (int c = 0; c < kSlabs; ++c)
+              tma_load(ring + slot * Sh::kTile + c * kSlab, j & 1 ? &v_map : &k_map, c * 64, w.head0 / a.gs,
+                       w.k0 + (j >> 1) * kN, &b.kv_full[slot]);
+            ++issued;
+          }
         }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+      if (!ok) {  // no copy may be in flight when the block ends
+        if (n_q > 0) wait_slow(&b.q_full, (n_q - 1) & 1, nullptr);
+        for (int x = max(0, issued - Sh::kStages); x < issued; ++x)
+          wait_slow(&b.kv_full[x % Sh::kStages], (x / Sh::kStages) & 1, nullptr);
       }
     } else if (warp == 8) {
       // ---- MMAs
-      if (n_max > 0) {
-        bool ok = wait_warp(&b.q_full, 0, &b.dead);
-        auto full = [&](int x) {
+      const uint64_t q_desc = desc(smem_u32(sm), 16), k_desc = desc(smem_u32(ring), 16), v_desc = desc(smem_u32(ring), kSlab);
+      uint32_t n_q = 0, taken = 0, step[2] = {0, 0};
+      for (uint32_t round = 0;; ++round) {
+        Item w;
+        if (!take(round, w)) break;
+        leave(round);
+        const int n0 = __shfl_sync(0xffffffffu, w.n[0], 0), n1 = __shfl_sync(0xffffffffu, w.n[1], 0), n_max = max(n0, n1);
+        if (n_max == 0) continue;
+        ok = wait_warp(&b.q_full, n_q++ & 1, &b.dead);
+        auto full = [&](uint32_t x) {  // the x-th load's place in the ring, in units of 16 bytes
           ok = ok && wait_warp(&b.kv_full[x % Sh::kStages], (x / Sh::kStages) & 1, &b.dead);
           return x % Sh::kStages * (Sh::kTile >> 4);
         };
-        auto release = [&](int x) {  // the last loads' slots are not filled again
-          if (x + Sh::kStages < 2 * n_max && elect()) dec::tc_commit(&b.kv_empty[x % Sh::kStages]);
+        auto release = [&](int x) {  // the item's x-th load's slot, if it will be filled again
+          if ((Sh::kStay || x + Sh::kStages < 2 * n_max) && elect()) dec::tc_commit(&b.kv_empty[(taken + x) % Sh::kStages]);
+          __syncwarp();
         };
-        const uint64_t q_desc = desc(smem_u32(sm), 16), k_desc = desc(smem_u32(ring), 16),
-                       v_desc = desc(smem_u32(ring), kSlab);
+        auto q_read = [&]() {
+          if (Sh::kStay && elect()) dec::tc_commit(&b.q_empty);
+          __syncwarp();
+        };
         auto scores = [&](int i, uint32_t kt) {
           if (elect()) {
 #pragma unroll
@@ -500,33 +595,64 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
           }
           __syncwarp();
         };
-        uint32_t kt = full(0);
-        if (ok) {
-          dec::tc_fence_after();
-          if (n0 > 0) scores(0, kt);
-          if (n1 > 0) scores(1, kt);
-          release(0);
-        }
+        uint32_t kt = full(taken);
+        if (!ok) break;
+        dec::tc_fence_after();
+        if (n0 > 0) scores(0, kt);
+        if (n1 > 0) scores(1, kt);
+        release(0);
+        if (n_max == 1) q_read();
         for (int j = 0; j < n_max && ok; ++j) {
-          const uint32_t vt = full(2 * j + 1);
-          if (j + 1 < n_max) kt = full(2 * j + 2);
+          const uint32_t vt = full(taken + 2 * j + 1);
+          if (j + 1 < n_max) kt = full(taken + 2 * j + 2);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int n = i ? n1 : n0;
             if (j >= n) continue;
-            ok = ok && wait_warp(&b.p_full[i], j & 1, &b.dead);
+            ok = ok && wait_warp(&b.p_full[i], step[i]++ & 1, &b.dead);
             if (!ok) break;
             dec::tc_fence_after();
             values(i, j, n, vt);
             if (j + 1 < n) scores(i, kt);
           }
           release(2 * j + 1);
-          release(2 * j + 2);
+          if (j + 1 < n_max) release(2 * j + 2);
+          if (j + 2 == n_max) q_read();
         }
-        if (!ok) {  // nor any MMA
-          if (elect()) dec::tc_commit(&b.drained);
-          wait_slow(&b.drained, 0, nullptr);
+        if (!ok) break;
+        taken += 2 * n_max;
+      }
+      if (Sh::kStay || !ok) {  // no MMA, and no arrival of one, may be under way when the block ends
+        if (elect()) dec::tc_commit(&b.drained);
+        __syncwarp();
+        wait_slow(&b.drained, 0, nullptr);
+      }
+    } else if (Sh::kStay && warp == 10) {
+      // ---- work: this block's own, then that of blocks which have not begun, one ahead of the other warps
+      int at = blockIdx.x;
+      uint32_t round = 0, asked = 0;
+      while (ok) {
+        if (at >= 0 && elect()) ask(&b.answer, &b.next);
+        __syncwarp();
+        Item w;
+        const bool some = at >= 0 && item_at(at, w);
+        if (some || at < 0) {
+          if (round > 1) ok = wait_warp(&b.item_empty[round & 1], (round >> 1) - 1 & 1, &b.dead);
+          if (at < 0) w.m0 = -1;
+          if (ok && lane == 0) {
+            b.item[round & 1] = w;
+            mbar_arrive(&b.item_full[round & 1]);
+          }
+          ++round;
         }
+        if (at < 0) break;
+        if (!__all_sync(0xffffffffu, wait_slow(&b.next, asked++ & 1, nullptr))) {  // an answer may not be under way either
+          b.dead = 1;
+          break;
+        }
+        at = answer_of(&b.answer);
+        dec::fence_async_smem();
+        __syncwarp();
       }
     }
   }
@@ -582,7 +708,7 @@ cudaError_t launch(const PrefillArgs& a, int n_seqs, cudaStream_t st) {
   }
   const int pair = a.gs % 2 == 0, rows_q = pair ? kM : 2 * kM;
   const int64_t blocks = (int64_t)n_seqs * ((a.max_q + rows_q - 1) / rows_q) * (pair ? a.heads / 2 : a.heads);
-  prefill_kernel<D><<<(unsigned)blocks, Sh::kThreads, Sh::kSmem, st>>>(q, k, v, a, n_seqs, pair);
+  prefill_kernel<D><<<(unsigned)blocks, Sh::kThreads, Sh::kSmem, st>>>(q, k, v, a, n_seqs, (int)blocks, pair);
   return cudaGetLastError();
 }
 
