@@ -405,7 +405,7 @@ int dec_attention_paged_workspace(const dec_paged_cache* cache, int32_t n_seqs, 
 /* Attention of one query token a sequence over its seq_lens[s] cached positions:
  * out[s][h] = softmax_t(scale * q[s][h] . K[t]) V[t], t < seq_lens[s]; zeros for an
  * empty sequence.  What the pages hold behind the length is never used.
- *   q, out     [n_seqs] rows, 16-byte aligned, strides multiples of 16 bytes
+ *   q, out     [n_seqs] rows, 16-byte aligned, strides multiples of 16 bytes; out does not overlap q
  *   workspace  dec_attention_paged_workspace bytes, 16-byte aligned, nothing to be initialised;
  *              calls that may overlap on the GPU need one each, calls in a row (captured or not) can share one
  * The results do not depend on scheduling: the same inputs give the same bits.
@@ -422,7 +422,7 @@ int dec_attention_paged(const dec_paged_cache* cache, int32_t dtype, const void*
  *   out[i][h] = softmax_t(scale * q[i][h] . k[t]) v[t]
  * Keys and values that a query does not see do not touch its result, whatever they
  * hold.  Rows of out behind the last sequence stay as they are.
- *   q, k, v, out  16-byte aligned, row strides multiples of 16 bytes
+ *   q, k, v, out  16-byte aligned, row strides multiples of 16 bytes; out overlaps none of the others
  *   n_q, n_k      rows of q (and out) and of k and v;  max_q: at least the longest query range
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int dec_attention_prefill(int32_t dtype, const void* q, const void* k, const void* v, void* out, int64_t q_stride,

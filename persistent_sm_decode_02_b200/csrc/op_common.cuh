@@ -25,6 +25,9 @@ inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 // A row stride must keep 16-byte loads aligned and rows apart.
 inline bool stride_ok(int64_t stride, int64_t row, int esz) { return stride >= row && (stride * esz) % 16 == 0; }
 
+// A softmax scale, in the base-2 units of the kernels too.
+inline bool scale_ok(float scale) { return scale > 0.f && isfinite(scale * 1.4426950408889634f); }
+
 inline int head_layout(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
   if (n_heads < 1 || n_kv_heads < 1 || head_dim < 1) return DEC_ERR_INVALID_ARG;
   if ((head_dim != 64 && head_dim != 128) || n_heads % n_kv_heads || n_heads / n_kv_heads > 8)

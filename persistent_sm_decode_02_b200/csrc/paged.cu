@@ -1068,13 +1068,13 @@ extern "C" int dec_attention_paged(const dec_paged_cache* cache, int32_t dtype, 
   size_t need = 0;
   int rc = dec_attention_paged_workspace(cache, n_seqs, n_heads, &need);
   if (rc) return rc;
-  if ((dtype != DEC_BF16 && dtype != DEC_F32) || !(scale > 0.f) || !isfinite(scale) || table_stride < 0)
+  if ((dtype != DEC_BF16 && dtype != DEC_F32) || !scale_ok(scale) || table_stride < 0)
     return DEC_ERR_INVALID_ARG;
   if (n_seqs == 0) return DEC_OK;
   const int hkv = cache->n_kv_heads, D = cache->head_dim, esz = dtype == DEC_BF16 ? 2 : 4;
   // tiles of 16 positions are counted in 32 bits
   if ((double)n_seqs * hkv * table_stride * cache->page_size / 16 >= 2147483648.0) return DEC_ERR_UNSUPPORTED;
-  if (!q || !out || !seq_lens || !page_table || !workspace || workspace_bytes < need) return DEC_ERR_INVALID_ARG;
+  if (!q || !out || !seq_lens || !page_table || !workspace || workspace_bytes < need || out == q) return DEC_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned4(seq_lens) || !aligned4(page_table) ||
       !aligned4(status) || !stride_ok(q_stride, (int64_t)n_heads * D, esz) ||
       !stride_ok(out_stride, (int64_t)n_heads * D, esz))

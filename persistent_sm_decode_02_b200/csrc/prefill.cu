@@ -184,7 +184,9 @@ __global__ void __launch_bounds__(256) prefill_fp32(PrefillArgs a, int tiles, in
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (ty * 4 + i >= rows) continue;
-    const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
+    // a row that sees nothing gives zeros, one that sees only scores of -infinity 0 / 0
+    const bool blind = n_end <= 0 || (a.causal && m0 + ty * 4 + i + shift < 0);
+    const float inv = blind ? 0.f : 1.f / l[i];
     float* op = static_cast<float*>(a.out) + (r.q0 + m0 + ty * 4 + i) * a.os + (int64_t)head * D;
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
@@ -213,11 +215,12 @@ extern "C" int dec_attention_prefill(int32_t dtype, const void* q, const void* k
                                      int32_t causal, float scale, int32_t* status, void* stream) {
   int rc = head_layout(n_heads, n_kv_heads, head_dim);
   if (rc) return rc;
-  if ((dtype != DEC_BF16 && dtype != DEC_F32) || !(scale > 0.f) || !isfinite(scale)) return DEC_ERR_INVALID_ARG;
+  if ((dtype != DEC_BF16 && dtype != DEC_F32) || !scale_ok(scale)) return DEC_ERR_INVALID_ARG;
   if (n_seqs < 0 || n_q < 0 || n_k < 0 || max_q < 0) return DEC_ERR_INVALID_ARG;
   if (n_seqs == 0 || n_q == 0 || max_q == 0) return DEC_OK;
   const int D = head_dim, esz = dtype == DEC_BF16 ? 2 : 4;
   if (!q || !out || !cu_q || !cu_k || (n_k > 0 && (!k || !v))) return DEC_ERR_INVALID_ARG;
+  if (out == q || out == k || out == v) return DEC_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned4(cu_q) || !aligned4(cu_k) ||
       !aligned4(status) || !stride_ok(q_stride, (int64_t)n_heads * D, esz) ||
       !stride_ok(out_stride, (int64_t)n_heads * D, esz) || !stride_ok(k_stride, (int64_t)n_kv_heads * D, esz) ||

@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
       const bool live = row < w.lq;
       const float inv = l != 0.f ? 1.f / l : 0.f;
       bf16* op = static_cast<bf16*>(a.out) + ((int64_t)w.q0 + row) * a.os + (int64_t)head * D;
-      bool bad = false;
+      bool bad = l == 0.f;  // (every score it sees was -infinity)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];

@@ -724,6 +724,30 @@ def test_prefill_unseen_keys_may_hold_anything(d, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_infinity(d, dtype):
+    """A query whose every score is -infinity, or any is +infinity, has no softmax: NaN, in its own row and head alone."""
+    h, hkv, n = 4, 2, 150
+    q, k, v = prefill_inputs(h, hkv, d, n, n, dtype, 45)
+    k = k.abs() + 0.5
+    q[40, 1], q[149, 3] = -math.inf, math.inf
+    out = torch.empty_like(q)
+    run_prefill(q, k, v, out, [n], [n], dtype)
+    bad = torch.isnan(out)
+    assert bool(bad[40, 1].all()) and bool(bad[149, 3].all()) and int(bad.sum()) == 2 * d
+    lens, ps = [90, 20], 32
+    pool = Pool(lens, hkv, d, ps, 46).fill(lens, 47)
+    pool.k &= 0x7F  # no negative keys
+    pool.k[pool.k == 0] = 0x20
+    x = q[:2].clone()
+    x[0, 1], x[1, 3] = -math.inf, math.inf
+    out = torch.empty_like(x)
+    run_paged(pool, x, out, lens, dtype)
+    bad = torch.isnan(out)
+    assert bool(bad[0, 1].all()) and bool(bad[1, 3].all()) and int(bad.sum()) == 2 * d
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prefill_large_scores(dtype):
     h, hkv, d, lens = 4, 2, 64, [300]
     for std, scale in ((12.0, None), (1e-3, None), (1.0, 0.5)):

@@ -32,14 +32,14 @@ def append(c=None, rope=None, **over):
 
 
 def attention(c=None, **over):
-    a = dict(dtype=D_.DEC_BF16, q=P, out=P, q_stride=256, out_stride=256, n_heads=4, n_seqs=1, seq_lens=P, page_table=P,
+    a = dict(dtype=D_.DEC_BF16, q=P, out=P + 4096, q_stride=256, out_stride=256, n_heads=4, n_seqs=1, seq_lens=P, page_table=P,
              table_stride=2, scale=0.125, workspace=P, workspace_bytes=1 << 30, status=None, stream=None)
     a.update(over)
     return D_.dec_attention_paged(cache() if c is None else c, *a.values())
 
 
 def prefill(**over):
-    a = dict(dtype=D_.DEC_BF16, q=P, k=P, v=P, out=P, q_stride=256, k_stride=128, v_stride=128, out_stride=256, n_heads=4,
+    a = dict(dtype=D_.DEC_BF16, q=P, k=P, v=P, out=P + 4096, q_stride=256, k_stride=128, v_stride=128, out_stride=256, n_heads=4,
              n_kv_heads=2, head_dim=64, n_seqs=1, n_q=3, n_k=3, max_q=3, cu_q=P, cu_k=P, causal=1, scale=0.125, status=None,
              stream=None)
     a.update(over)
@@ -100,15 +100,15 @@ def test_heads_are_checked(over, rc):
 
 @pytest.mark.parametrize("over", [dict(dtype=2), dict(q=None), dict(out=None), dict(seq_lens=None), dict(page_table=None),
                                   dict(workspace=None), dict(workspace_bytes=0), dict(workspace=P + 8), dict(q=P + 8),
-                                  dict(out=P + 2), dict(seq_lens=P + 2), dict(q_stride=255), dict(out_stride=260),
+                                  dict(out=P + 2), dict(out=P), dict(seq_lens=P + 2), dict(q_stride=255), dict(out_stride=260),
                                   dict(n_seqs=-1), dict(table_stride=-1), dict(scale=0.0), dict(scale=-1.0),
-                                  dict(scale=float("nan")), dict(scale=float("inf"))], ids=str)
+                                  dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38)], ids=str)
 def test_attention_is_checked(over):
     assert attention(**over) == INVALID
 
 
 @pytest.mark.parametrize("over,rc", [(dict(dtype=2), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID),
-                                     (dict(v=None), INVALID), (dict(out=None), INVALID), (dict(cu_q=None), INVALID),
+                                     (dict(v=None), INVALID), (dict(out=None), INVALID), (dict(out=P), INVALID), (dict(cu_q=None), INVALID),
                                      (dict(cu_k=P + 2), INVALID), (dict(q=P + 8), INVALID), (dict(k_stride=120), INVALID),
                                      (dict(v_stride=129), INVALID), (dict(n_q=-1), INVALID), (dict(max_q=-1), INVALID),
                                      (dict(n_k=-1), INVALID), (dict(n_seqs=-1), INVALID), (dict(head_dim=80), UNSUPPORTED),
