@@ -97,6 +97,20 @@ __device__ __forceinline__ void rotate16(float* x, const float* cs, const float*
   }
 }
 
+// Whether x, which is up to two units in the last place off where nothing cancels, lies at the middle between two E4M3
+// values: the scales are powers of two, so that shows in the 20 bits which a code does not keep.
+__device__ __forceinline__ bool at_border(float x) {
+  return (__float_as_uint(x) << 12) + ((2u - 0x80000u) << 12) <= (4u << 12);  // at most 2 units from 0x80000
+}
+
+// Rotated keys at a border (one block in three has any), noted on the way and stored again at the block's end from an fp64
+// rotation: the codes are then as near to the exact values as a rounding can be, where fp32's last bit would decide.
+struct Border {
+  int head, row, unit;
+  float raw[16];
+};
+constexpr int kBorders = 32;  // more than that keep what fp32 gave
+
 __device__ __forceinline__ void store_codes(uint8_t* p, const float* x, float inv) {
   uint2 o;
   o.x = e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16);
@@ -162,12 +176,14 @@ __device__ __forceinline__ void angles(const AppendArgs& a, int c, int64_t pos, 
 
 // Blocks of a (sequence, page it touches): some for its kv heads, some for its query heads.  A thread holds the same 16
 // dims of its rows for every head, so it computes their 8 angles once.  Bound by memory where tokens are many (4 x 8192
-// tokens, 32 / 8 heads of 128, bf16: 738 MB in 138 us, 5.3 TB/s), by the chain of dependent loads (offsets, page id,
-// row) where they are few (one token 3.8 us).  A page's scale needs all of its new values, so its keys and values stay in
+// tokens, 32 / 8 heads of 128, bf16: 738 MB in 142 us, 5.2 TB/s), by the chain of dependent loads (offsets, page id,
+// row) where they are few (one token 4.0 us).  A page's scale needs all of its new values, so its keys and values stay in
 // registers between the maximum and the rounding and are read once; the next head's are on their way meanwhile.
 template <typename T, int D, int NIT, int ROLE>
 __device__ __forceinline__ void append_block(const AppendArgs& a) {
   __shared__ float red[2][2][16];
+  __shared__ int borders;
+  __shared__ Border border_s[kBorders];
   constexpr int kUnits = D / 16;  // threads a row
   constexpr int kBatch = 4;       // query heads whose loads are under way at once
   const int blocks = (ROLE & kKeysValues ? a.kv_blocks : 0) + (ROLE & kQueries ? a.q_blocks : 0);
@@ -241,7 +257,9 @@ __device__ __forceinline__ void append_block(const AppendArgs& a) {
         vr[it][1].load(vp + d1);
       }
   };
+  if (tid == 0) borders = 0;
   load(g0);
+  __syncthreads();
   for (int head = g0; head < g1; ++head) {
     float k[NIT][16], mk = 0.f, mv = 0.f;
     Vec8<T> v[NIT][2];
@@ -250,7 +268,20 @@ __device__ __forceinline__ void append_block(const AppendArgs& a) {
       if (row[it] < nr) {
         kr[it][0].get(k[it]);
         kr[it][1].get(k[it] + 8);
-        if (turned) rotate16(k[it], cs[it], sn[it], neighbour);
+        if (turned) {
+          rotate16(k[it], cs[it], sn[it], neighbour);
+          bool border = false;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) border |= at_border(k[it][i]);
+          if (border) {
+            const int at = atomicAdd(&borders, 1);
+            if (at < kBorders) {
+              border_s[at].head = head, border_s[at].row = row[it], border_s[at].unit = c;
+              kr[it][0].get(border_s[at].raw);
+              kr[it][1].get(border_s[at].raw + 8);
+            }
+          }
+        }
         if (a.k_out) {
           T* op = static_cast<T*>(a.k_out) + (row0 + row[it]) * a.kos + (int64_t)head * D;
           Vec8<T>::store(op + d0, k[it]);
@@ -309,6 +340,22 @@ __device__ __forceinline__ void append_block(const AppendArgs& a) {
         store_codes(vp + at + d1, y + 8, iv);
       }
     __syncthreads();  // red is used again
+  }
+  if (!page_ok) return;
+  for (int e = tid; e < min(borders, kBorders) * 16; e += blockDim.x) {
+    const Border& b = border_s[e >> 4];
+    const int j = e & 15, i = neighbour ? j >> 1 : j & 7;
+    const bool second = neighbour ? j & 1 : j >> 3;
+    const double turns = (double)(p.lo + b.row) * a.inv_freq[8 * b.unit + i] * 0.15915494309189535;
+    double sn64, cs64;
+    sincospi(2.0 * (turns - rint(turns)), &sn64, &cs64);
+    const double x = b.raw[neighbour ? 2 * i : i], y = b.raw[neighbour ? 2 * i + 1 : i + 8];
+    const double r = (second ? x * sn64 + y * cs64 : x * cs64 - y * sn64) * a.factor;
+    const float f = __double2float_rz(r);  // rounded to odd: an inexact result has its last bit set
+    const float z = (double)f != r ? __uint_as_float(__float_as_uint(f) | 1u) : f;
+    const int64_t si = (int64_t)page * a.c.hkv + b.head;
+    const int dim = neighbour ? 16 * b.unit + j : 8 * b.unit + (second ? a.rot / 2 : 0) + i;
+    a.c.k[(si * ps + slot0 + b.row) * D + dim] = (uint8_t)e4m3x2(z * (1.f / a.c.ks[si]), 0.f);
   }
 }
 
