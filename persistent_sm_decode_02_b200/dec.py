@@ -378,7 +378,7 @@ _ERR_TEXT = {DEC_ERR_INVALID_ARG: "bad pointer, size, stride or enum value", DEC
 
 
 def _chk_op(name, rc):
-    if rc != DEC_OK:
+    if rc:
         raise DecError(rc, f"{name}: {_ERR_TEXT.get(rc, 'error')}")
 
 
@@ -388,21 +388,24 @@ class PagedCache:
     1/sqrt(head_dim); stream is a cudaStream_t (None: the legacy default stream)."""
 
     def __init__(self, k_pages, v_pages, k_scales, v_scales, *, n_pages, page_size, n_kv_heads, head_dim):
+        self.lib = load_library()
         self.c = dec_paged_cache(k_pages, v_pages, k_scales, v_scales, n_pages, page_size, n_kv_heads, head_dim)
+        self.head_dim, self.kv_row, self.scale = head_dim, n_kv_heads * head_dim, max(1, head_dim) ** -0.5
 
     def append(self, q, k, v, q_out, cu_new, seq_lens, page_table, *, table_stride, n_seqs, n_tokens, max_new, n_heads,
                dtype=DEC_BF16, strides=None, inv_freq=None, rot_dim=0, neighbour_pairs=False, factor=1.0, k_out=None,
                k_out_stride=None, status=None, stream=None):
         """dec_kv_append; strides: (q, k, v, q_out).  q and q_out may be None: keys and values alone; k_out: where the
         rotated keys are wanted, too."""
-        kv = self.c.n_kv_heads * self.c.head_dim
         if strides is None:
-            row = n_heads * self.c.head_dim
-            strides = (row, kv, kv, row)
-        rope = dec_rope(inv_freq, rot_dim, DEC_ROPE_NEIGHBOUR if neighbour_pairs else DEC_ROPE_HALF, factor)
-        _chk_op("dec_kv_append", dec_kv_append(self.c, rope, dtype, q, k, v, q_out, k_out, *strides,
-                                               kv if k_out_stride is None else k_out_stride, n_heads, n_seqs, n_tokens,
-                                               max_new, cu_new, seq_lens, page_table, table_stride, status, stream))
+            row = n_heads * self.head_dim
+            strides = (row, self.kv_row, self.kv_row, row)
+        rc = self.lib.dec_kv_append(self.c, dec_rope(inv_freq, rot_dim, DEC_ROPE_NEIGHBOUR if neighbour_pairs else DEC_ROPE_HALF, factor), dtype, q, k,
+                                    v, q_out, k_out, *strides, self.kv_row if k_out_stride is None else k_out_stride,
+                                    n_heads, n_seqs, n_tokens, max_new, cu_new, seq_lens, page_table, table_stride, status,
+                                    stream)
+        if rc:
+            _chk_op("dec_kv_append", rc)
 
     def workspace_bytes(self, n_seqs, n_heads) -> int:
         n = ctypes.c_size_t(0)
@@ -413,12 +416,13 @@ class PagedCache:
     def attention(self, q, out, seq_lens, page_table, *, table_stride, n_seqs, n_heads, workspace, workspace_bytes,
                   dtype=DEC_BF16, q_stride=None, out_stride=None, scale=None, status=None, stream=None):
         """dec_attention_paged."""
-        row = n_heads * self.c.head_dim
-        _chk_op("dec_attention_paged",
-                dec_attention_paged(self.c, dtype, q, out, row if q_stride is None else q_stride,
-                                    row if out_stride is None else out_stride, n_heads, n_seqs, seq_lens, page_table,
-                                    table_stride, self.c.head_dim ** -0.5 if scale is None else scale, workspace,
-                                    workspace_bytes, status, stream))
+        row = n_heads * self.head_dim
+        rc = self.lib.dec_attention_paged(self.c, dtype, q, out, row if q_stride is None else q_stride,
+                                          row if out_stride is None else out_stride, n_heads, n_seqs, seq_lens, page_table,
+                                          table_stride, self.scale if scale is None else scale, workspace, workspace_bytes,
+                                          status, stream)
+        if rc:
+            _chk_op("dec_attention_paged", rc)
 
 
 def attention_prefill(q, k, v, out, cu_q, cu_k, *, n_seqs, n_q, n_k, max_q, n_heads, n_kv_heads, head_dim,
@@ -427,7 +431,8 @@ def attention_prefill(q, k, v, out, cu_q, cu_k, *, n_seqs, n_q, n_k, max_q, n_he
     scale defaults to 1/sqrt(head_dim)."""
     if strides is None:
         strides = (n_heads * head_dim, n_kv_heads * head_dim, n_kv_heads * head_dim, n_heads * head_dim)
-    _chk_op("dec_attention_prefill",
-            dec_attention_prefill(dtype, q, k, v, out, *strides, n_heads, n_kv_heads, head_dim, n_seqs, n_q, n_k, max_q,
-                                  cu_q, cu_k, int(causal), head_dim ** -0.5 if scale is None else scale, status,
-                                  stream))
+    rc = load_library().dec_attention_prefill(dtype, q, k, v, out, *strides, n_heads, n_kv_heads, head_dim, n_seqs, n_q, n_k,
+                                              max_q, cu_q, cu_k, 1 if causal else 0,
+                                              (max(1, head_dim) ** -0.5) if scale is None else scale, status, stream)
+    if rc:
+        _chk_op("dec_attention_prefill", rc)
