@@ -416,10 +416,10 @@ cudaError_t launch_append(const AppendArgs& a, int64_t pages, int units, bool sp
 // 2^(s + log2 vs - m'), with a running maximum m' of their own, and the sum uses 2^(s - m).  Either maximum moves
 // only when a score is 2^10 above it (weights then reach 2^14, inside fp16), so most tiles need no reduction.
 //
-// Bound by memory for large batches: 128 sequences of up to 8192, 32 / 8 heads of 128, 1.26 GB in 228 us, 5.5 TB/s (84 %
+// Bound by memory for large batches: 128 sequences of up to 8192, 32 / 8 heads of 128, 1.26 GB in 221-230 us, 5.5-5.7 TB/s (85 %
 // of the measured copy; blocks with equal work end between 185 and 230 us, as the SMs' shares of the bandwidth differ).
 // Every warp has three tiles' copies under way, which covers the latency without a barrier between warps.  Small calls are
-// latency: 8.7 us for one sequence of 77, 16.9 us for one of 8193, of which 2-3 us find the place on the line and as much
+// latency: 7.2 us for one sequence of 77, 16.4 us for one of 8193, of which 2-3 us find the place on the line and as much
 // joins; a third of a small call's stalls are first fetches of instructions, so what runs once is kept short.
 constexpr int kBlocks = 148;  // one block per SM of a B200
 constexpr int kWarps = 12;
@@ -604,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
   // the first `more` warps have each + 1 tiles, the others `each`
   const unsigned blocks = min((total + kLeast * kWarps - 1) / (kLeast * kWarps), (unsigned)kBlocks);
   if (blockIdx.x >= blocks) return;
-  const unsigned warps = blocks * kWarps, each = total / warps, more = total - each * warps;
+  const unsigned warps = min(blocks * kWarps, (total + kLeast - 1) / kLeast), each = total / warps, more = total - each * warps;
   const unsigned begin = gw * each + min((unsigned)gw, more);
-  int left = (int)(each + (gw < more));
+  int left = gw < warps ? (int)(each + (gw < more)) : 0;
   Place get;
   if (left > 0) {
     unsigned at = 0;  // where the sequence begins on the line
@@ -866,8 +866,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
   const uint32_t below = used & ((1u << lane) - 1);
   const int prev = below ? 31 - __clz(below) : 0;
   const int px = __shfl_sync(0xffffffffu, mine_o.x, prev), py = __shfl_sync(0xffffffffu, mine_o.y, prev);
-  uint32_t starts = __ballot_sync(0xffffffffu, mine_o.x >= 0 && (!below || px != mine_o.x || py != mine_o.y));
+  const uint32_t starts = __ballot_sync(0xffffffffu, mine_o.x >= 0 && (!below || px != mine_o.x || py != mine_o.y));
   if (!starts) return;
+  // lane i, where a run starts at slot i: its slots and kind
+  const uint32_t later = starts & ~((2u << lane) - 1);
+  const uint32_t slots = used & ~((1u << lane) - 1) & (later ? (1u << (__ffs(later) - 1)) - 1 : 0xFFFFFFFFu);
+  const bool ends = __shfl_sync(0xffffffffu, mine_o.z, 31 - __clz(slots | 1)) & 2;
+  const bool is_start = starts >> lane & 1, late = ends && !(mine_o.z & 1), few = !late && __popc(slots) <= 4;
+  uint32_t shorts = __ballot_sync(0xffffffffu, is_start && few), longs = __ballot_sync(0xffffffffu, is_start && !few && !late),
+           waiting = __ballot_sync(0xffffffffu, is_start && late);
   auto slot_at = [&](int k) {
     return k & 1 ? reinterpret_cast<const float*>(sm + (k >> 1) * Sh::kRing)
                  : reinterpret_cast<const float*>(sm + kWarps * Sh::kRing + (k >> 1) * Sh::kSlot);
@@ -875,17 +882,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
   constexpr int kItems = 8 * (D / 4);  // (head, four dims)
   // Short runs first, a warp each; then long ones, by all warps; last the one that waits for earlier blocks, so that what
   // a block hands on never waits for what it is handed.
-  for (int pass = 0; pass < 3; ++pass) {
-    uint32_t todo = starts;
-    for (int run = 0; todo; ++run) {
-      const int i0 = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const uint32_t members = used & ~((1u << i0) - 1) & (todo ? (1u << (__ffs(todo) - 1)) - 1 : 0xFFFFFFFFu);
-      const int4 fst = open_s[i0], lst = open_s[31 - __clz(members)];
-      const bool from_start = fst.z & 1, to_end = lst.z & 2, waits = !from_start && to_end;
+  for (int run = 0; shorts | longs | waiting; ++run) {
+    const bool shorter = shorts;
+    uint32_t& from = shorts ? shorts : longs ? longs : waiting;
+    const int i0 = __ffs(from) - 1;
+    from &= from - 1;
+    if (shorter && run % kWarps != warp) continue;
+    {
+      const uint32_t members = __shfl_sync(0xffffffffu, slots, i0);
+      const int4 fst = open_s[i0];
+      const bool from_start = fst.z & 1, to_end = __shfl_sync(0xffffffffu, ends, i0), waits = to_end && !from_start;
       const int first = waits ? fst.w : blockIdx.x, local = __popc(members);  // blocks first .. this one - 1 have parts of it
-      const bool shorter = !waits && local <= 4;
-      if (pass != (waits ? 2 : shorter ? 0 : 1) || (shorter && run % kWarps != warp)) continue;
       float* part = a.part + (size_t)(2 * blockIdx.x + from_start) * (24 + 8 * D);
       auto put = [&](int h, int d, const float (&x)[4], float M, float Mp, float l) {
         if (to_end) {
@@ -994,8 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
         if (tid == 0 && late_s) flag(a.status, DEC_SEQ_TIMEOUT);
       }
       if (!to_end && (shorter ? lane == 0 : tid == 0)) {
-        __threadfence();
-        store_release(a.ready + 2 * blockIdx.x + from_start, a.key);
+        store_release(a.ready + 2 * blockIdx.x + from_start, a.key);  // behind the barrier above, hence every thread's part
       }
     }
   }
