@@ -677,7 +677,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // This lane's share of a (sequence, head)'s queries: head g's dims 64 c + 16 t on.  The first is under way with the copies
+  // (in fp32 there are no registers to hold it).
+  Vec8<T> q_raw[kRow][2];
+  auto q_at = [&](int c) { return static_cast<const T*>(a.q) + use.s * a.qs + ((int64_t)use.head * a.gs + g) * D + 64 * c + 16 * t; };
+  auto load_q = [&]() {
+    if (g < a.gs)
+#pragma unroll
+      for (int c = 0; c < kRow; ++c) q_raw[c][0].load(q_at(c)), q_raw[c][1].load(q_at(c) + 8);
+  };
   look_up();
+  if (!kPair && left > 0) load_q();
 #pragma unroll 1
   for (int i = 0; i < Sh::kStages - 1; ++i) fetch();
 
@@ -688,18 +698,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
     uint32_t qh[kSteps][2], ql[kPair ? kSteps : 1][2];
     float f0, f1;  // score factors of this lane's two heads, 2t and 2t + 1
     {
-      const T* qp = static_cast<const T*>(a.q) + use.s * a.qs + ((int64_t)use.head * a.gs + g) * D;
       float x[kRow][16], mx = 0.f;
 #pragma unroll
       for (int c = 0; c < kRow; ++c) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[c][i] = 0.f;
         if (g < a.gs) {
-          Vec8<T> w;
-          w.load(qp + 64 * c + 16 * t);
-          w.get(x[c]);
-          w.load(qp + 64 * c + 16 * t + 8);
-          w.get(x[c] + 8);
+          if (kPair) q_raw[c][0].load(q_at(c));
+          q_raw[c][0].get(x[c]);
+          if (kPair) q_raw[c][1].load(q_at(c) + 8);
+          q_raw[c][1].get(x[c] + 8);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) mx = amax_finite(mx, x[c][i]);
@@ -856,6 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
     use.tile = tiles - 1;
     if (left > 0) use.next(a);
     if (use.s >= a.n_seqs) left = 0;
+    if (!kPair && left > 0) load_q();
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
