@@ -16,13 +16,21 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool live) 
 __device__ __forceinline__ void earlier_copies() { asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory"); }
 
 // fp32 prompts, on the CUDA cores (the tensor cores' fp32 inputs keep 11 bits).  A block takes 32 queries of one head,
-// and its two groups of 4 warps every other 64 keys, so that the longest row's chain of steps is short; each keeps the
-// running maximum and sum of its softmax, and they are joined at the end.  A thread has 4 x 4 scores and 4 x (D / 16)
+// and its groups of 4 warps 64 keys in turn, so that the longest row's chain of steps is short; each keeps the running
+// maximum and sum of its softmax, and they are joined at the end.  A block has an SM to itself: short rows then go where
+// long ones are done, not beside them.  A thread has 4 x 4 scores and 4 x (D / 16)
 // outputs, in pairs for the two-wide FMA.  K of a group's next step is on its way while this one's values are added up,
-// V while its scores are worked out.  Five ragged prompts of up to 700, 4 heads of 64: 50 us (64 queries and one group: 87).
+// V while its scores are worked out.  Five ragged prompts of up to 700, 4 heads of 64: 39 us (two
+// groups and two blocks an SM 51, one group and 64 queries 87).
 template <int D>
-__global__ void __launch_bounds__(256) prefill_fp32(PrefillArgs a, int tiles, int n_seqs) {
-  constexpr int kM = 32, kN = 64, kStride = D + 4, kC = D / 64;
+struct Fp32Shape {
+  static constexpr int kGroups = D == 64 ? 4 : 2;  // what shared memory holds
+  static constexpr int kSmem = (32 * (D + 4) + kGroups * (2 * 64 * (D + 4) + 32 * 64)) * 4;
+};
+
+template <int D>
+__global__ void __launch_bounds__(Fp32Shape<D>::kGroups * 128) prefill_fp32(PrefillArgs a, int tiles, int n_seqs) {
+  constexpr int kM = 32, kN = 64, kStride = D + 4, kC = D / 64, kGroups = Fp32Shape<D>::kGroups, kStep = kGroups * kN;
   extern __shared__ __align__(16) float sm[];
   constexpr int kGroup = 2 * kN * kStride + kM * kN;  // floats of a group: K, V, P
   const int group = threadIdx.x >> 7;
@@ -51,7 +59,7 @@ __global__ void __launch_bounds__(256) prefill_fp32(PrefillArgs a, int tiles, in
     asm volatile("cp.async.commit_group;" ::: "memory");
     load(v_s, a.v, a.vs, group * kN);
   }
-  for (int e = threadIdx.x; e < kM * (D / 4); e += 256) {
+  for (int e = threadIdx.x; e < kM * (D / 4); e += kGroups * 128) {
     const int i = e / (D / 4), c = e % (D / 4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i < rows) x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (r.q0 + m0 + i) * a.qs + (int64_t)head * D + c);
@@ -67,7 +75,7 @@ __global__ void __launch_bounds__(256) prefill_fp32(PrefillArgs a, int tiles, in
     for (int c = 0; c < kC * 2; ++c) o[i][c] = 0;
   }
   __syncthreads();
-  for (int n0 = group * kN; n0 < n_end; n0 += 2 * kN) {
+  for (int n0 = group * kN; n0 < n_end; n0 += kStep) {
     earlier_copies();  // K is here, V may be under way
     sync();
     F2 sc2[4][4];  // sums over even and odd dims
@@ -92,7 +100,7 @@ __global__ void __launch_bounds__(256) prefill_fp32(PrefillArgs a, int tiles, in
       sc[i / 4][i % 4] = u.x + u.y;
     }
     sync();  // K is read
-    if (n0 + 2 * kN < n_end) load(k_s, a.k, a.ks, n0 + 2 * kN);
+    if (n0 + kStep < n_end) load(k_s, a.k, a.ks, n0 + kStep);
     int seen[4];  // keys of this tile that row i sees
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -154,32 +162,37 @@ __global__ void __launch_bounds__(256) prefill_fp32(PrefillArgs a, int tiles, in
         if (t < seen[i]) add(i, p_s[(ty * 4 + i) * kN + t], y);  // an unseen value may be anything
     }
     sync();  // V is read
-    if (n0 + 2 * kN < n_end) {
+    if (n0 + kStep < n_end) {
       asm volatile("cp.async.commit_group;" ::: "memory");
-      load(v_s, a.v, a.vs, n0 + 2 * kN);
+      load(v_s, a.v, a.vs, n0 + kStep);
     }
   }
-  // the second group's sums to the first, through its K and V tiles
-  float* x_s = q_s + kM * kStride + kGroup;
-  if (group == 1) {
+  // the other groups' sums to the first, through their K and V tiles
+  if (group > 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int c = 0; c < kC * 2; ++c) reinterpret_cast<F2*>(x_s)[(i * kC * 2 + c) * 128 + tid] = o[i][c];
-      x_s[(16 * kC + i) * 128 + tid] = m[i], x_s[(16 * kC + 4 + i) * 128 + tid] = l[i];
+      for (int c = 0; c < kC * 2; ++c) reinterpret_cast<F2*>(k_s)[(i * kC * 2 + c) * 128 + tid] = o[i][c];
+      k_s[(16 * kC + i) * 128 + tid] = m[i], k_s[(16 * kC + 4 + i) * 128 + tid] = l[i];
     }
   }
   __syncthreads();
-  if (group == 1) return;
+  if (group > 0) return;
+#pragma unroll 1
+  for (int other = 1; other < kGroups; ++other) {
+    const float* x_s = k_s + other * kGroup;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float m1 = x_s[(16 * kC + i) * 128 + tid], l1 = x_s[(16 * kC + 4 + i) * 128 + tid];
-    const float mn = fmaxf(m[i], m1), base = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(m[i] - base), f1 = exp2f(m1 - base);
-    l[i] = l[i] * f + l1 * f1;
+    for (int i = 0; i < 4; ++i) {
+      const float m1 = x_s[(16 * kC + i) * 128 + tid], l1 = x_s[(16 * kC + 4 + i) * 128 + tid];
+      const float mn = fmaxf(m[i], m1), base = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m[i] - base), f1 = exp2f(m1 - base);
+      m[i] = mn;
+      l[i] = l[i] * f + l1 * f1;
 #pragma unroll
-    for (int c = 0; c < kC * 2; ++c)
-      o[i][c] = tc::fma2(reinterpret_cast<F2*>(x_s)[(i * kC * 2 + c) * 128 + tid], tc::f2(f1, f1), tc::mul2(o[i][c], tc::f2(f, f)));
+      for (int c = 0; c < kC * 2; ++c)
+        o[i][c] = tc::fma2(reinterpret_cast<const F2*>(x_s)[(i * kC * 2 + c) * 128 + tid], tc::f2(f1, f1),
+                           tc::mul2(o[i][c], tc::f2(f, f)));
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -199,10 +212,11 @@ __global__ void __launch_bounds__(256) prefill_fp32(PrefillArgs a, int tiles, in
 template <int D>
 cudaError_t launch_fp32(const PrefillArgs& a, int n_seqs, cudaStream_t st) {
   const int tiles = (a.max_q + 31) / 32;
-  const int smem = (32 * (D + 4) + 2 * (2 * 64 * (D + 4) + 32 * 64)) * 4;
+  constexpr int smem = Fp32Shape<D>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(prefill_fp32<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  prefill_fp32<D><<<(unsigned)((int64_t)n_seqs * tiles * a.heads), 256, smem, st>>>(a, tiles, n_seqs);
+  prefill_fp32<D><<<(unsigned)((int64_t)n_seqs * tiles * a.heads), Fp32Shape<D>::kGroups * 128, smem, st>>>(
+      a, tiles, n_seqs);
   return cudaGetLastError();
 }
 
