@@ -421,7 +421,8 @@ int dec_attention_paged(const dec_paged_cache* cache, int32_t dtype, const void*
  * one before it one fewer, and so on; a query that sees no key gets zeros.
  *   out[i][h] = softmax_t(scale * q[i][h] . k[t]) v[t]
  * Keys and values that a query does not see do not touch its result, whatever they
- * hold.  Rows of out behind the last sequence stay as they are.
+ * hold.  Rows of out behind the last sequence stay as they are.  In a batch of mostly
+ * short sequences an entry of cu_q that is inconsistent leaves out all of them.
  *   q, k, v, out  16-byte aligned, row strides multiples of 16 bytes; out overlaps none of the others
  *   n_q, n_k      rows of q (and out) and of k and v;  max_q: at least the longest query range
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */

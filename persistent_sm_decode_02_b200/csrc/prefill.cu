@@ -29,19 +29,25 @@ struct Fp32Shape {
 };
 
 template <int D>
-__global__ void __launch_bounds__(Fp32Shape<D>::kGroups * 128) prefill_fp32(PrefillArgs a, int tiles, int n_seqs) {
+__global__ void __launch_bounds__(Fp32Shape<D>::kGroups * 128) prefill_fp32(PrefillArgs a, Tiling tl, int n_seqs) {
   constexpr int kM = 32, kN = 64, kStride = D + 4, kC = D / 64, kGroups = Fp32Shape<D>::kGroups, kStep = kGroups * kN;
   extern __shared__ __align__(16) float sm[];
   constexpr int kGroup = 2 * kN * kStride + kM * kN;  // floats of a group: K, V, P
   const int group = threadIdx.x >> 7;
   float *q_s = sm, *k_s = q_s + kM * kStride + group * kGroup, *v_s = k_s + kN * kStride, *p_s = v_s + kN * kStride;
   auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };
-  const int head = blockIdx.x % a.heads, s = blockIdx.x / a.heads % n_seqs;
-  const int tile = tiles - 1 - blockIdx.x / a.heads / n_seqs;  // long rows first
+  const int head = blockIdx.x % a.heads;
+  int m0;
+  const int at = blockIdx.x / a.heads;
+  const int s = tl.packed ? tile_at<true>(a, n_seqs, tl.tiles, kM, at, m0) : tile_at<false>(a, n_seqs, tl.tiles, kM, at, m0);
+  if (s < 0) {
+    if (threadIdx.x == 0) flag(a.status, DEC_SEQ_BAD_RANGE);
+    return;
+  }
   const int tid = threadIdx.x & 127, tx = tid & 15, ty = tid >> 4;
   const Range r = range_of(a, s);
   if (!r.ok && threadIdx.x == 0) flag(a.status, DEC_SEQ_BAD_RANGE);
-  const int m0 = tile * kM, kvh = head / a.gs;
+  const int kvh = head / a.gs;
   if (m0 >= r.lq) return;
   const int rows = min(kM, r.lq - m0), shift = r.lk - r.lq;
   const int n_end = !r.ok ? 0 : a.causal ? min(r.lk, m0 + rows + shift) : r.lk;
@@ -211,12 +217,12 @@ __global__ void __launch_bounds__(Fp32Shape<D>::kGroups * 128) prefill_fp32(Pref
 
 template <int D>
 cudaError_t launch_fp32(const PrefillArgs& a, int n_seqs, cudaStream_t st) {
-  const int tiles = (a.max_q + 31) / 32;
+  const Tiling tl = tiling(n_seqs, a.n_q, a.max_q, 32);
   constexpr int smem = Fp32Shape<D>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(prefill_fp32<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  prefill_fp32<D><<<(unsigned)((int64_t)n_seqs * tiles * a.heads), Fp32Shape<D>::kGroups * 128, smem, st>>>(
-      a, tiles, n_seqs);
+  prefill_fp32<D><<<(unsigned)((int64_t)tl.tiles * (tl.packed ? 1 : n_seqs) * a.heads), Fp32Shape<D>::kGroups * 128, smem, st>>>(
+      a, tl, n_seqs);
   return cudaGetLastError();
 }
 

@@ -60,6 +60,43 @@ __device__ __forceinline__ Range range_of(const PrefillArgs& a, int s) {
   return r;
 }
 
+// How queries are cut into tiles of `rows`.  Sequences of about one length: as many tiles for each as the longest has, the
+// late ones of all sequences first.  Where that would leave most of them empty: tile t of the whole batch, sequence s
+// owning those from cu_q[s] / rows + s on (never fewer than it needs), late sequences first.
+struct Tiling {
+  int tiles, packed;  // tiles of a sequence, or of the batch
+};
+inline Tiling tiling(int n_seqs, int n_q, int max_q, int rows) {
+  const int64_t each = ((int64_t)max_q + rows - 1) / rows, batch = (int64_t)n_q / rows + n_seqs;
+  // 8 prompts of 4096 among 500 of up to 100, 32 heads of 128: 1.39 ms packed, 1.63 with 32 tiles for each; of 64: 1.29, 2.97.
+  // Of about one length, the plain cut's order (longest rows of all sequences first) ends more evenly.
+  return n_seqs * each > 4 * batch ? Tiling{(int)batch, 1} : Tiling{(int)each, 0};
+}
+// Tile `at` of the launch (on a whole warp): its sequence and first query.  packed: -1 where an offset is out of order,
+// as every later one would be off.
+template <bool kPacked>
+__device__ __forceinline__ int tile_at(const PrefillArgs& a, int n_seqs, int tiles, int rows, int at, int& m0) {
+  if (!kPacked) {
+    m0 = (tiles - 1 - at / n_seqs) * rows;
+    return at % n_seqs;
+  }
+  const int t = tiles - 1 - at, lane = threadIdx.x & 31;
+  int s = -1, first = 0;
+  bool sound = true;
+#pragma unroll 1
+  for (int i = lane; i - lane < n_seqs; i += 32) {
+    const int q0 = i < n_seqs ? a.cu_q[i] : 0, q1 = i < n_seqs ? a.cu_q[i + 1] : 0;
+    sound &= q0 >= 0 && q1 >= q0 && q1 <= a.n_q;
+    const uint32_t own = __ballot_sync(0xffffffffu, i < n_seqs && q0 / rows + i <= t);
+    if (own) {
+      s = i - lane + 31 - __clz(own);
+      first = __shfl_sync(0xffffffffu, q0 / rows + i, 31 - __clz(own));
+    }
+  }
+  m0 = s < 0 ? 1 << 30 : (t - first) * rows;  // before the first sequence: past its end
+  return __all_sync(0xffffffffu, sound) ? max(s, 0) : -1;
+}
+
 namespace tc {
 
 using dec::mbar_arrive;
@@ -293,10 +330,10 @@ __device__ __forceinline__ void redo_row(const PrefillArgs& a, const __nv_bfloat
   for (int i = 0; i < kD; ++i) out[lane * kD + i] = __float2bfloat16_rn(o[i] / l);
 }
 
-template <int D>
+template <int D, bool kPacked>
 __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                   const __grid_constant__ CUtensorMap v_map, const PrefillArgs a, const int n_seqs, const int items,
+                   const __grid_constant__ CUtensorMap v_map, const PrefillArgs a, const int n_seqs, const int tiles,
                    const int pair) {
   using Sh = Shape<D>;
   using bf16 = __nv_bfloat16;
@@ -309,11 +346,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
   // Work `at` of the launch.  pair: the tiles are heads 2x and 2x + 1; else queries m0 and m0 + 128.  Late queries, with
   // most keys, first.  false: the sequence ends before it.
   auto item_at = [&](int at, Item& w) {
-    const int s = at / columns % n_seqs;
+    const int s = tile_at<kPacked>(a, n_seqs, tiles, pair ? kM : 2 * kM, at / columns, w.m0);
+    if (kPacked && s < 0) {
+      if (lane == 0) flag(a.status, DEC_SEQ_BAD_RANGE);
+      return false;
+    }
     const Range r = range_of(a, s);
     w.q0 = (int)r.q0, w.k0 = (int)r.k0, w.lq = r.lq, w.lk = r.lk, w.sound = r.ok;
     w.head0 = (pair ? 2 : 1) * (at % columns);
-    w.m0 = (items / columns / n_seqs - 1 - at / columns / n_seqs) * (pair ? kM : 2 * kM);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // steps of a tile, up to the last key its last row sees
       const int mi = w.m0 + i * mstep;
@@ -687,6 +727,24 @@ inline bool make_map(CUtensorMap* m, const void* base, int rows, int heads, int 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int D, bool kPacked>
+cudaError_t start(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PrefillArgs& a, int n_seqs,
+                  int tiles, int pair, unsigned blocks, cudaStream_t st) {
+  using Sh = Shape<D>;
+  cudaError_t e =
+      cudaFuncSetAttribute(prefill_kernel<D, kPacked>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  if (e != cudaSuccess) return e;
+  if (D == 128) {
+    static const int regs = [] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, prefill_kernel<D, kPacked>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs != Sh::kRegs) return cudaErrorInvalidValue;  // the warps would wait for registers that are not there
+  }
+  prefill_kernel<D, kPacked><<<blocks, Sh::kThreads, Sh::kSmem, st>>>(q, k, v, a, n_seqs, tiles, pair);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch(const PrefillArgs& a, int n_seqs, cudaStream_t st) {
   using Sh = Shape<D>;
@@ -697,19 +755,11 @@ cudaError_t launch(const PrefillArgs& a, int n_seqs, cudaStream_t st) {
   if (!make_map(&q, a.q, a.n_q, a.heads, D, a.qs, kM) || !make_map(&k, kp, rows, heads, D, keys ? a.ks : a.qs, Sh::kN) ||
       !make_map(&v, vp, rows, heads, D, keys ? a.vs : a.qs, Sh::kN))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
-  if (e != cudaSuccess) return e;
-  if (D == 128) {
-    static const int regs = [] {
-      cudaFuncAttributes f;
-      return cudaFuncGetAttributes(&f, prefill_kernel<D>) == cudaSuccess ? f.numRegs : 0;
-    }();
-    if (regs != Sh::kRegs) return cudaErrorInvalidValue;  // the warps would wait for registers that are not there
-  }
   const int pair = a.gs % 2 == 0, rows_q = pair ? kM : 2 * kM;
-  const int64_t blocks = (int64_t)n_seqs * ((a.max_q + rows_q - 1) / rows_q) * (pair ? a.heads / 2 : a.heads);
-  prefill_kernel<D><<<(unsigned)blocks, Sh::kThreads, Sh::kSmem, st>>>(q, k, v, a, n_seqs, (int)blocks, pair);
-  return cudaGetLastError();
+  const Tiling tl = tiling(n_seqs, a.n_q, a.max_q, rows_q);
+  const int64_t blocks = (int64_t)tl.tiles * (tl.packed ? 1 : n_seqs) * (pair ? a.heads / 2 : a.heads);
+  return tl.packed ? start<D, true>(q, k, v, a, n_seqs, tl.tiles, pair, (unsigned)blocks, st)
+                   : start<D, false>(q, k, v, a, n_seqs, tl.tiles, pair, (unsigned)blocks, st);
 }
 
 }  // namespace tc

@@ -724,6 +724,28 @@ def test_prefill_unseen_keys_may_hold_anything(d, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("h,hkv,d", [(4, 2, 64), (3, 1, 128), (8, 2, 128)])
+def test_prefill_one_long_among_many_short(h, hkv, d, dtype):
+    """Tiles of the whole batch, not as many for each as the longest has; rows before the first sequence; empty ones."""
+    lens = [(3 * i) % 7 for i in range(250)] + [1500] + [129, 0, 128] + [(5 * i) % 4 for i in range(250)]
+    before = 300
+    n = before + sum(lens)
+    q, k, v = prefill_inputs(h, hkv, d, n, n, dtype, 48)
+    out = torch.full((n + 1, h, d), 7.0, dtype=q.dtype, device="cuda")
+    cu, status = ints([before + a for a in offsets(lens)]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    run_prefill(q, k, v, out, cu, cu, dtype, max_q=1500, status=status)
+    check_prefill(q[before:], k[before:], v[before:], out[before:], lens, lens, dtype)
+    assert int(status) == 0 and bool((out[:before] == 7.0).all()) and bool((out[n:] == 7.0).all())
+    # an offset out of order leaves such a batch out whole
+    bad = cu.clone()
+    bad[100] = before - 1
+    out.fill_(7.0)
+    run_prefill(q, k, v, out, bad, cu, dtype, max_q=1500, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == D_.DEC_SEQ_BAD_RANGE and bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_scores_of_infinity(d, dtype):
     """A query whose every score is -infinity, or any is +infinity, has no softmax: NaN, in its own row and head alone."""
