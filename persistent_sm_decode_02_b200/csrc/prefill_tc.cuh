@@ -513,9 +513,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
       leave(round);
       const int row = w.m0 + i * mstep + (tid & 127), head = w.head0 + (pair ? i : 0);
       const bool live = row < w.lq;
-      const float inv = l != 0.f ? 1.f / l : 0.f;
+      // No score above -infinity.  (The sum does not tell: the polynomial gives such a score 2^-126.)
+      const bool none = m == -INFINITY || l == 0.f;
+      const float inv = none ? 0.f : 1.f / l;
       bf16* op = static_cast<bf16*>(a.out) + ((int64_t)w.q0 + row) * a.os + (int64_t)head * D;
-      bool bad = l == 0.f;  // (every score it sees was -infinity)
+      bool bad = none;  // where it sees any, NaN
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
           float y[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            y[k] = l != 0.f ? __uint_as_float(o[e + k]) * inv : 0.f;
+            y[k] = none ? 0.f : __uint_as_float(o[e + k]) * inv;
             bad |= !(fabsf(y[k]) <= 3.38953139e38f);  // bf16's largest: not finite, or rounding to infinity
           }
           if (live) Vec8<bf16>::store(op + c * 32 + e, y);
