@@ -415,6 +415,8 @@ cudaError_t launch_append(const AppendArgs& a, int64_t pages, int units, bool sp
 // Scales: a tile lies in one page, so K's scale multiplies its scores, and V's enters the exponent: weights are
 // 2^(s + log2 vs - m'), with a running maximum m' of their own, and the sum uses 2^(s - m).  Either maximum moves
 // only when a score is 2^10 above it (weights then reach 2^14, inside fp16), so most tiles need no reduction.
+// A maximum of -infinity means that no position was seen; one of the lowest finite value, that every score seen was
+// -infinity (those weigh nothing beside a finite score, and alone they have no softmax).
 //
 // Bound by memory for large batches: 128 sequences of up to 8192, 32 / 8 heads of 128, 1.26 GB in 221-230 us, 5.5-5.7 TB/s (85 %
 // of the measured copy; blocks with equal work end between 185 and 230 us, as the SMs' shares of the bandwidth differ).
@@ -519,9 +521,9 @@ struct PagedShape {
 // Weights of an open end in a join: 2^(m - M), nothing where the end saw no position.
 __device__ __forceinline__ float join_weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
 
-// O / l in the units of V: O counts 2^(M' - 4), l counts 2^M.
+// O / l in the units of V: O counts 2^(M' - 4), l counts 2^M.  Without a weight: 0 where no position was seen, else NaN.
 __device__ __forceinline__ float unit(float l, float M, float Mp) {
-  return l == 0.f ? 0.f : ex2(Mp - M - 4.f) / l;
+  return l == 0.f ? (M == -INFINITY ? 0.f : NAN) : ex2(Mp - M - 4.f) / l;
 }
 
 __device__ __forceinline__ uint64_t clock_ns() {
@@ -765,8 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
       const bool in0 = g < rows, in1 = g + 8 < rows;
       const float s0 = (c[0][0] + c[1][0]) * k0, s1 = (c[0][1] + c[1][1]) * k1;
       const float s2 = (c[0][2] + c[1][2]) * k0, s3 = (c[0][3] + c[1][3]) * k1;
-      const float x0 = fmaxf(in0 ? s0 : -INFINITY, in1 ? s2 : -INFINITY);
-      const float x1 = fmaxf(in0 ? s1 : -INFINITY, in1 ? s3 : -INFINITY);
+      const float least = in0 ? -FLT_MAX : -INFINITY;
+      const float x0 = fmaxf(fmaxf(in0 ? s0 : least, in1 ? s2 : least), least);
+      const float x1 = fmaxf(fmaxf(in0 ? s1 : least, in1 ? s3 : least), least);
       if (__any_sync(0xffffffffu, x0 > m0 + 10.f || x0 + lv > n0 + 10.f || x1 > m1 + 10.f || x1 + lv > n1 + 10.f)) {
         float y0 = x0, y1 = x1;
 #pragma unroll

@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import test_gpu_operators as ops
-from test_gpu_operators import run_prefill
+from persistent_sm_decode_02_b200 import dec as D_
+from test_gpu_operators import DT, U, Pool, gen, run_paged, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +36,51 @@ def test_prefill_rows_whose_every_score_is_minus_infinity(kind, d, causal, dtype
     run_prefill(q, k, v, out, [n], [n], dtype, causal)
     assert bool(torch.isnan(out[bad]).all())
     assert torch.equal(out[~bad], clean[~bad])
+
+
+# ------------------------------------------------------------------------------------------------ paged attention
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,first", [(40, 16), (40, 17), (33, 32), (600, 100), (600, 590), (9000, 4000), (40, 40), (9000, 9000)])
+def test_paged_scores_that_overflow_weigh_nothing(n, first, dtype):
+    """The first positions' scores pass fp32's range (-infinity), the others' are 0: the mean of the others' values, to the
+    rounding of equal weights (none: powers of two) and their sum; NaN where there are no others."""
+    h, hkv, d, ps = 4, 2, 64, 16
+    pool = Pool([n, n], hkv, d, ps, 210).fill([n, n], 211)
+    for b in range(2):
+        ids = pool.table[b].long()
+        pool.k[ids, :, :, 0] = 0
+        flat = torch.arange(len(ids) * ps, device="cuda").view(-1, ps)
+        low = (flat < first)[:, None, :].expand(-1, hkv, -1)
+        page = pool.k[ids]
+        page[..., 0] = torch.where(low, 0x7E, 0).to(torch.uint8)  # 448
+        pool.k[ids] = page
+        pool.ks[ids] = 2.0 ** 30
+    q = torch.zeros(2, h, d, device="cuda")
+    q[0, :, 0] = -1e30  # score -1e30 * 448 * 2^30 / 8
+    q = q.to(DT[dtype][0])
+    out = torch.empty_like(q)
+    run_paged(pool, q, out, [n, n], dtype)
+    if first == n:
+        assert bool(torch.isnan(out[0]).all())
+    else:
+        _, v = pool.rows(0, n)
+        v = v[:, first:].repeat_interleave(h // hkv, 0)
+        ref, a = v.mean(1), v.abs().mean(1)
+        assert bool(((out[0].double() - ref).abs() <= DT[dtype][2] * ref.abs() + a * (2.0 ** -20 + n * U)).all())
+    _, v = pool.rows(1, n)  # scores of 0 throughout
+    v = v.repeat_interleave(h // hkv, 0)
+    ref, a = v.mean(1), v.abs().mean(1)
+    assert bool(((out[1].double() - ref).abs() <= DT[dtype][2] * ref.abs() + a * (2.0 ** -20 + n * U)).all())
+
+
+def test_paged_no_page_to_read_gives_zeros():
+    """A sequence whose every page id is bad has no position to see."""
+    h, hkv, d, ps, lens = 4, 2, 64, 16, [40, 700]
+    pool = Pool(lens, hkv, d, ps, 212).fill(lens, 213)
+    table = pool.table.clone()
+    table[1] = pool.n_pages
+    q = torch.randn(2, h, d, generator=gen(214), device="cuda")
+    out, status = torch.full_like(q, 7.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+    run_paged(pool, q, out, lens, "f32", table=table, status=status)
+    assert int(status) == D_.DEC_SEQ_BAD_PAGE and bool((out[1] == 0).all())
+    ops.check_paged(pool, q[:1], out[:1], lens[:1], "f32")
