@@ -405,16 +405,20 @@ cudaError_t launch_append(const AppendArgs& a, int64_t pages, int units, bool sp
 // behind them, so it never waits for a block that has no SM.)  Sums are in the order of the line: the same bits every time.
 //
 // A warp computes S^T = K q^T (16 positions x 8 query heads) and O^T += V^T P (D x 8) with m16n8k16 fp16 MMAs.
-// E4M3 codes are exact in fp16; q is scaled by a power of two into fp16's upper range, where a bf16 q is exact; the
-// weights are rounded to fp16 (2^-11, well below a bf16 result's own rounding).  For fp32, q and the weights are
-// pairs of fp16 (22 bits) and each product two MMAs.  Positions as M and heads as N waste nothing for a group of 8.
+// E4M3 codes are exact in fp16; q is scaled by a power of two into fp16's upper range, where a bf16 q is exact (an element
+// is off by at most 2^-39 of the largest); the weights are rounded to fp16 (2^-11, well below a bf16 result's own
+// rounding).  For fp32, q and the weights are pairs of fp16 and each product two MMAs; a q element has 22 bits or 2^-39 of the
+// largest.  The low half of a pair of weights is held 2^12 higher and meets V 2^12 lower, which for E4M3 values is exact in
+// fp16 too.  Positions as M and heads as N waste nothing for a group of 8.
 // An MMA's K index may be permuted freely, so a lane's four bytes of a K row are the k pairs (2t, 2t+1) and
 // (2t+8, 2t+9) of one MMA, and 16-byte shared-memory reads feed it without a shuffle; V^T pairs positions, one
 // byte permute a word.  The weights, in the accumulator's layout, become the second MMA's operand by movmatrix.
 //
 // Scales: a tile lies in one page, so K's scale multiplies its scores, and V's enters the exponent: weights are
-// 2^(s + log2 vs - m'), with a running maximum m' of their own, and the sum uses 2^(s - m).  Either maximum moves
-// only when a score is 2^10 above it (weights then reach 2^14, inside fp16), so most tiles need no reduction.
+// 2^(s + log2 vs - m' + 13), with a running maximum m' of their own, and the sum uses 2^(s - m).  m' moves only when a
+// score is 2^2 above it, so most tiles need no reduction, and weights stay below 2^15, inside fp16.  Down to 2^-27 of the
+// largest they have fp16's 11 bits, and down to 2^-30 a pair has 20; below, one is off by at most 2^-38 of the largest, a pair by
+// 2^-50.
 // A maximum of -infinity means that no position was seen; one of the lowest finite value, that every score seen was
 // -infinity (those weigh nothing beside a finite score, and alone they have no softmax).
 //
@@ -490,10 +494,16 @@ __device__ __forceinline__ uint32_t pack_half(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// What rounding (x, y) to the halves in h left over.
-__device__ __forceinline__ uint32_t pack_rest(float x, float y, uint32_t h) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack_half(x - f.x, y - f.y);
+// What rounding (x, y) to the halves in h left over, times f.
+__device__ __forceinline__ uint32_t pack_rest(float x, float y, uint32_t h, float f = 1.f) {
+  const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_half((x - z.x) * f, (y - z.y) * f);
+}
+// Two halves times 1 / kLow.
+__device__ __forceinline__ uint32_t lower(uint32_t x) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x0C000C00u));  // 2^-12
+  return y;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -518,12 +528,16 @@ struct PagedShape {
   static_assert(kRing >= kSlot && kSmem <= 227 * 1024 - 24 * 1024, "shared memory");
 };
 
+constexpr float kTop = 13.f;   // log2 of the weight of a score at the maximum
+constexpr float kGrow = 2.f;   // how far a score may be above it: weights stay below 2^(kTop + kGrow), fp16 ends at 2^16
+constexpr float kLow = 4096.f; // what a pair's low half, at most 2^(kTop + kGrow - 12), is multiplied by
+
 // Weights of an open end in a join: 2^(m - M), nothing where the end saw no position.
 __device__ __forceinline__ float join_weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
 
-// O / l in the units of V: O counts 2^(M' - 4), l counts 2^M.  Without a weight: 0 where no position was seen, else NaN.
+// O / l in the units of V: O counts 2^(M' - 13), l counts 2^M.  Without a weight: 0 where no position was seen, else NaN.
 __device__ __forceinline__ float unit(float l, float M, float Mp) {
-  return l == 0.f ? (M == -INFINITY ? 0.f : NAN) : ex2(Mp - M - 4.f) / l;
+  return l == 0.f ? (M == -INFINITY ? 0.f : NAN) : ex2(Mp - M - kTop) / l;
 }
 
 __device__ __forceinline__ uint64_t clock_ns() {
@@ -770,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
       const float least = in0 ? -FLT_MAX : -INFINITY;
       const float x0 = fmaxf(fmaxf(in0 ? s0 : least, in1 ? s2 : least), least);
       const float x1 = fmaxf(fmaxf(in0 ? s1 : least, in1 ? s3 : least), least);
-      if (__any_sync(0xffffffffu, x0 > m0 + 10.f || x0 + lv > n0 + 10.f || x1 > m1 + 10.f || x1 + lv > n1 + 10.f)) {
+      if (__any_sync(0xffffffffu, x0 > m0 + kGrow || x0 + lv > n0 + kGrow || x1 > m1 + kGrow || x1 + lv > n1 + kGrow)) {
         float y0 = x0, y1 = x1;
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) {
@@ -785,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
         for (int i = 0; i < kSteps; ++i) o[i][0] *= w0, o[i][1] *= w1, o[i][2] *= w0, o[i][3] *= w1;
         m0 = a0, m1 = a1, n0 = b0, n1 = b1;
       }
-      const float b0 = lv + 4.f - (n0 == -INFINITY ? 0.f : n0), b1 = lv + 4.f - (n1 == -INFINITY ? 0.f : n1);
+      const float b0 = lv + kTop - (n0 == -INFINITY ? 0.f : n0), b1 = lv + kTop - (n1 == -INFINITY ? 0.f : n1);
       const float p0 = in0 ? ex2(s0 + b0) : 0.f, p1 = in0 ? ex2(s1 + b1) : 0.f;
       const float p2 = in1 ? ex2(s2 + b0) : 0.f, p3 = in1 ? ex2(s3 + b1) : 0.f;
       l0 += (in0 ? ex2(s0 - m0) : 0.f) + (in1 ? ex2(s2 - m0) : 0.f);
@@ -793,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
       const uint32_t h0 = pack_half(p0, p1), h1 = pack_half(p2, p3);
       const uint32_t ph0 = transpose8x8(h0), ph1 = transpose8x8(h1);
       uint32_t pl0 = 0, pl1 = 0;
-      if (kPair) pl0 = transpose8x8(pack_rest(p0, p1, h0)), pl1 = transpose8x8(pack_rest(p2, p3, h1));
+      if (kPair) pl0 = transpose8x8(pack_rest(p0, p1, h0, kLow)), pl1 = transpose8x8(pack_rest(p2, p3, h1, kLow));
       // V: this lane's D / 8 dims of positions 2t, 2t + 1, 2t + 8, 2t + 9
       uint32_t v[4][D / 32];
 #pragma unroll
@@ -814,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
         const uint32_t u = __byte_perm(v[0][i / 2], v[1][i / 2], sel), w = __byte_perm(v[2][i / 2], v[3][i / 2], sel);
         const uint32_t a0 = half_codes(u), a1 = half_codes(u >> 16), a2 = half_codes(w), a3 = half_codes(w >> 16);
         mma16816(o[i], a0, a1, a2, a3, ph0, ph1);
-        if (kPair) mma16816(o[i], a0, a1, a2, a3, pl0, pl1);
+        if (kPair) mma16816(o[i], lower(a0), lower(a1), lower(a2), lower(a3), pl0, pl1);
       }
     }
 #pragma unroll

@@ -84,3 +84,34 @@ def test_paged_no_page_to_read_gives_zeros():
     run_paged(pool, q, out, lens, "f32", table=table, status=status)
     assert int(status) == D_.DEC_SEQ_BAD_PAGE and bool((out[1] == 0).all())
     ops.check_paged(pool, q[:1], out[:1], lens[:1], "f32")
+
+
+@pytest.mark.parametrize("dtype,down", [("bf16", 20), ("bf16", 26), ("f32", 20), ("f32", 29)])
+def test_paged_small_weights_keep_their_bits(dtype, down):
+    """One key takes the weight and has the value zero; what is left are weights about 2^-down of it.  Sequences as many as
+    there are pieces of the line, so that one piece sees both."""
+    h, hkv, d, ps, n, n_seqs = 4, 1, 64, 16, 63 * 16, 1776
+    pool = Pool([32], hkv, d, ps, 220).fill([32], 221)
+    strong, weak = (int(x) for x in pool.table[0])
+    pool.table = torch.full((n_seqs, n // ps), weak, dtype=torch.int32, device="cuda")
+    pool.table[:, 0] = strong
+    pool.width, pool.n_pages = n // ps, pool.k.shape[0]
+    pool.k[[strong, weak]] = 0
+    pool.k[strong, :, 5, 0] = 0x38  # 1
+    pool.v[strong] = 0
+    pool.ks[[strong, weak]] = 1.0
+    pool.vs[[strong, weak]] = 1.0
+    score = torch.linspace(down - 1, down, 37, dtype=torch.float64, device="cuda") * math.log(2)
+    q = torch.zeros(n_seqs, h, d, device="cuda")
+    q[:, :, 0] = (score[torch.arange(n_seqs, device="cuda") % 37] * 8).float()[:, None]
+    q = q.to(DT[dtype][0])
+    out = torch.empty_like(q)
+    run_paged(pool, q, out, [n] * n_seqs, dtype)
+    w = torch.exp(-q[:, :, 0].double() / 8)  # of each of the others, against the one's 1
+    _, v = pool.rows(0, 32)
+    ref = (w * (n // ps - 1))[..., None] * v[0, 16:].sum(0) / (1 + w * (n - 1))[..., None]
+    a = (w * (n // ps - 1))[..., None] * v[0, 16:].abs().sum(0) / (1 + w * (n - 1))[..., None]
+    # a score is off by (scaling by log2 e, the hardware's 2^x) 2 u of itself
+    tol = DT[dtype][2] * ref.abs() + a * ((2.0 ** -11 if dtype == "bf16" else 2.0 ** -20) + 4 * U * down + 2.0 ** -20 + n * U)
+    err = (out.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
