@@ -98,18 +98,22 @@ __device__ __forceinline__ void rotate16(float* x, const float* cs, const float*
 }
 
 // Whether x, which is up to two units in the last place off where nothing cancels, lies at the middle between two E4M3
-// values: the scales are powers of two, so that shows in the 20 bits which a code does not keep.
+// values: the scales are powers of two, so that shows in the 20 bits which a code of normal size does not keep.  (Middles
+// between subnormal codes, of values below 2^-15 of the page's largest, are not looked for.)
 __device__ __forceinline__ bool at_border(float x) {
   return (__float_as_uint(x) << 12) + ((2u - 0x80000u) << 12) <= (4u << 12);  // at most 2 units from 0x80000
 }
 
-// Rotated keys at a border (one block in three has any), noted on the way and stored again at the block's end from an fp64
-// rotation: the codes are then as near to the exact values as a rounding can be, where fp32's last bit would decide.
-struct Border {
-  int head, row, unit;
-  float raw[16];
-};
-constexpr int kBorders = 32;  // more than that keep what fp32 gave
+// Rotated keys with a value at a border between two codes of normal size (a block of 8 heads of a page of 64 in three has
+// any) are noted, a bit for a thread's 16 values, and done again at the block's end from an fp64 rotation: their codes are
+// then the exact values' nearest, where fp32's last bit would decide.  Their place in k_out, which may be k, is written
+// there too.  Where the angles are 0 and the factor is 1 fp32 is exact, and nothing is noted.
+__device__ __forceinline__ bool exact_turn(const float* cs, const float* sn) {
+  bool exact = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) exact &= sn[i] == 0.f && fabsf(cs[i]) == 1.f;
+  return exact;
+}
 
 __device__ __forceinline__ void store_codes(uint8_t* p, const float* x, float inv) {
   uint2 o;
@@ -182,8 +186,7 @@ __device__ __forceinline__ void angles(const AppendArgs& a, int c, int64_t pos, 
 template <typename T, int D, int NIT, int ROLE>
 __device__ __forceinline__ void append_block(const AppendArgs& a) {
   __shared__ float red[2][2][16];
-  __shared__ int borders;
-  __shared__ Border border_s[kBorders];
+  extern __shared__ uint32_t border_s[];  // [heads of the block][NIT][warps]: lanes whose key values are at a border
   constexpr int kUnits = D / 16;  // threads a row
   constexpr int kBatch = 4;       // query heads whose loads are under way at once
   const int blocks = (ROLE & kKeysValues ? a.kv_blocks : 0) + (ROLE & kQueries ? a.q_blocks : 0);
@@ -239,11 +242,18 @@ __device__ __forceinline__ void append_block(const AppendArgs& a) {
   const int g0 = a.c.hkv * part / a.kv_blocks, g1 = a.c.hkv * (part + 1) / a.kv_blocks;
   float cs[NIT][8], sn[NIT][8];
   int row[NIT];
+  bool watch[NIT];
 #pragma unroll
   for (int it = 0; it < NIT; ++it) {
     row[it] = (tid + it * blockDim.x) / kUnits;
-    if (turned && row[it] < nr) angles(a, c, p.lo + row[it], sn[it], cs[it]);
+    watch[it] = false;
+    if (turned && row[it] < nr) {
+      angles(a, c, p.lo + row[it], sn[it], cs[it]);
+      watch[it] = page_ok && !exact_turn(cs[it], sn[it]);
+    }
   }
+  const int warps = blockDim.x >> 5, warp = tid >> 5, lane = tid & 31;
+  uint32_t any = 0;
   Vec8<T> kr[NIT][2], vr[NIT][2];
   auto load = [&](int head) {
 #pragma unroll
@@ -257,32 +267,23 @@ __device__ __forceinline__ void append_block(const AppendArgs& a) {
         vr[it][1].load(vp + d1);
       }
   };
-  if (tid == 0) borders = 0;
   load(g0);
-  __syncthreads();
   for (int head = g0; head < g1; ++head) {
     float k[NIT][16], mk = 0.f, mv = 0.f;
     Vec8<T> v[NIT][2];
 #pragma unroll
-    for (int it = 0; it < NIT; ++it)
+    for (int it = 0; it < NIT; ++it) {
+      bool border = false;
       if (row[it] < nr) {
         kr[it][0].get(k[it]);
         kr[it][1].get(k[it] + 8);
         if (turned) {
           rotate16(k[it], cs[it], sn[it], neighbour);
-          bool border = false;
 #pragma unroll
           for (int i = 0; i < 16; ++i) border |= at_border(k[it][i]);
-          if (border) {
-            const int at = atomicAdd(&borders, 1);
-            if (at < kBorders) {
-              border_s[at].head = head, border_s[at].row = row[it], border_s[at].unit = c;
-              kr[it][0].get(border_s[at].raw);
-              kr[it][1].get(border_s[at].raw + 8);
-            }
-          }
+          border &= watch[it];
         }
-        if (a.k_out) {
+        if (a.k_out && !border) {
           T* op = static_cast<T*>(a.k_out) + (row0 + row[it]) * a.kos + (int64_t)head * D;
           Vec8<T>::store(op + d0, k[it]);
           Vec8<T>::store(op + d1, k[it] + 8);
@@ -298,6 +299,10 @@ __device__ __forceinline__ void append_block(const AppendArgs& a) {
           mv = fmaxf(mv, fabsf(y[i]));
         }
       }
+      const uint32_t noted = __ballot_sync(0xffffffffu, border);
+      if (lane == 0) border_s[((head - g0) * NIT + it) * warps + warp] = noted;
+      any |= noted;
+    }
     if (head + 1 < g1) load(head + 1);
     if (!page_ok) continue;
     const int64_t si = (int64_t)page * a.c.hkv + head;
@@ -341,21 +346,40 @@ __device__ __forceinline__ void append_block(const AppendArgs& a) {
       }
     __syncthreads();  // red is used again
   }
-  if (!page_ok) return;
-  for (int e = tid; e < min(borders, kBorders) * 16; e += blockDim.x) {
-    const Border& b = border_s[e >> 4];
-    const int j = e & 15, i = neighbour ? j >> 1 : j & 7;
-    const bool second = neighbour ? j & 1 : j >> 3;
-    const double turns = (double)(p.lo + b.row) * a.inv_freq[8 * b.unit + i] * 0.15915494309189535;
-    double sn64, cs64;
-    sincospi(2.0 * (turns - rint(turns)), &sn64, &cs64);
-    const double x = b.raw[neighbour ? 2 * i : i], y = b.raw[neighbour ? 2 * i + 1 : i + 8];
-    const double r = (second ? x * sn64 + y * cs64 : x * cs64 - y * sn64) * a.factor;
-    const float f = __double2float_rz(r);  // rounded to odd: an inexact result has its last bit set
-    const float z = (double)f != r ? __uint_as_float(__float_as_uint(f) | 1u) : f;
-    const int64_t si = (int64_t)page * a.c.hkv + b.head;
-    const int dim = neighbour ? 16 * b.unit + j : 8 * b.unit + (second ? a.rot / 2 : 0) + i;
-    a.c.k[(si * ps + slot0 + b.row) * D + dim] = (uint8_t)e4m3x2(z * (1.f / a.c.ks[si]), 0.f);
+  if (!any) return;
+  const int words = (g1 - g0) * NIT;  // of this warp
+  for (int w0 = 0; w0 < words; w0 += 32) {
+    const uint32_t bits = w0 + lane < words ? border_s[(w0 + lane) * warps + warp] : 0;
+    for (uint32_t some = __ballot_sync(0xffffffffu, bits != 0); some; some &= some - 1) {
+      const int from = __ffs(some) - 1, head = g0 + (w0 + from) / NIT, it = (w0 + from) % NIT;
+      // two threads' values at a time, one a lane
+      for (uint32_t left = __shfl_sync(0xffffffffu, bits, from); left;) {
+        const int b0 = __ffs(left) - 1;
+        left &= left - 1;
+        const int b1 = left ? __ffs(left) - 1 : b0;
+        left &= left - 1;
+        const int t = warp * 32 + (lane < 16 ? b0 : b1) + it * blockDim.x, r = t / kUnits, u = t % kUnits;
+        const int j = lane & 15, i = neighbour ? j >> 1 : j & 7;
+        const bool second = neighbour ? j & 1 : j >> 3;
+        const int first = neighbour ? 16 * u + 2 * i : 8 * u + i, apart = neighbour ? 1 : a.rot / 2;
+        const T* kp = static_cast<const T*>(a.k) + (row0 + r) * a.ks + (int64_t)head * D + first;
+        const double x = (double)(float)kp[0], y = (double)(float)kp[apart];
+        const double turns = (double)(p.lo + r) * a.inv_freq[8 * u + i] * 0.15915494309189535;
+        double sn64, cs64;
+        sincospi(2.0 * (turns - rint(turns)), &sn64, &cs64);
+        const double v = (second ? x * sn64 + y * cs64 : x * cs64 - y * sn64) * a.factor;
+        const float f = __double2float_rz(v);  // rounded to odd: an inexact result has its last bit set
+        const float z = (double)f != v ? __uint_as_float(__float_as_uint(f) | 1u) : f;
+        const int64_t si = (int64_t)page * a.c.hkv + head;
+        const int dim = first + (second ? apart : 0);
+        a.c.k[(si * ps + slot0 + r) * D + dim] = (uint8_t)e4m3x2(z * (1.f / a.c.ks[si]), 0.f);
+        __syncwarp();  // k is read: k_out may be k
+        if (a.k_out) {
+          T* op = static_cast<T*>(a.k_out) + (row0 + r) * a.kos + (int64_t)head * D + dim;
+          if (sizeof(T) == 4) *op = (T)__double2float_rn(v); else *op = (T)z;
+        }
+      }
+    }
   }
 }
 
@@ -373,12 +397,13 @@ template <typename T, int D>
 cudaError_t launch_append(const AppendArgs& a, int64_t pages, int units, bool split, cudaStream_t s) {
   const int nit = units > 512 ? 2 : 1;
   const int threads = ((units + nit - 1) / nit + 31) / 32 * 32;
+  const int notes = (a.c.hkv + a.kv_blocks - 1) / a.kv_blocks * nit * (threads / 32) * 4;
   if (!split) {
     const int blocks = (int)(pages * (a.kv_blocks + a.q_blocks));
     if (nit == 2)
-      append_kernel<T, D, 2, kBoth><<<blocks, threads, 0, s>>>(a);
+      append_kernel<T, D, 2, kBoth><<<blocks, threads, notes, s>>>(a);
     else
-      append_kernel<T, D, 1, kBoth><<<blocks, threads, 0, s>>>(a);
+      append_kernel<T, D, 1, kBoth><<<blocks, threads, notes, s>>>(a);
     return cudaGetLastError();
   }
   append_kernel<T, D, 1, kQueries><<<(int)(pages * a.q_blocks), threads < 256 ? threads : 256, 0, s>>>(a);
@@ -387,6 +412,7 @@ cudaError_t launch_append(const AppendArgs& a, int64_t pages, int units, bool sp
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((int)(pages * a.kv_blocks));
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = notes;
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1115,7 +1141,8 @@ extern "C" int dec_kv_append(const dec_paged_cache* cache, const dec_rope* rope,
   // 4 x 8192 154 (one launch) / 138 (two), 64 x 4 tokens 5.0 / 9.8.
   const bool split = q && units >= 256;
   const int64_t enough = split ? 2 * 148 : 8 * 148;
-  while (a.kv_blocks > 1 && pages * a.kv_blocks > enough) a.kv_blocks = (a.kv_blocks + 1) / 2;
+  // (a block notes borders in shared memory: 128 bytes a head, which is enough for 128 heads)
+  while (a.kv_blocks > 1 && pages * a.kv_blocks > enough && hkv <= a.kv_blocks / 2 * 128) a.kv_blocks = (a.kv_blocks + 1) / 2;
   while (a.q_blocks > 1 && pages * a.q_blocks > enough) a.q_blocks = (a.q_blocks + 1) / 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;

@@ -9,7 +9,7 @@ import torch
 
 import test_gpu_operators as ops
 from persistent_sm_decode_02_b200 import dec as D_
-from test_gpu_operators import DT, U, Pool, gen, run_paged, run_prefill
+from test_gpu_operators import DT, U, Pool, gen, run_append, run_paged, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,112 @@ def test_paged_small_weights_keep_their_bits(dtype, down):
     tol = DT[dtype][2] * ref.abs() + a * ((2.0 ** -11 if dtype == "bf16" else 2.0 ** -20) + 4 * U * down + 2.0 ** -20 + n * U)
     err = (out.double() - ref).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+# ------------------------------------------------------------------------------------------------ append
+def _border_keys(rows, hkv, d, pos, fr, pairs, factor, dtype, seed):
+    """Keys whose rotation is as near as the type allows to the middles between E4M3 codes (scale 1: one value of 400 a
+    head), the two of a pair in one binade."""
+    g = gen(seed)
+    r = d // 2
+    shape = (rows, hkv, r)
+    e = torch.randint(-3, 7, shape, generator=g, device="cuda").double()
+    x, y = (torch.ldexp((8.5 + torch.randint(0, 7, shape, generator=g, device="cuda").double()) / 8, e)
+            * (torch.randint(0, 2, shape, generator=g, device="cuda") * 2 - 1) for _ in range(2))
+    i = torch.arange(r, device="cuda")
+    i, j = (i, i + r) if pairs == "half" else (2 * i, 2 * i + 1)
+    c, s = (f(pos.double()[:, None, None] * fr) / factor for f in (torch.cos, torch.sin))
+    k = torch.empty(rows, hkv, d, dtype=torch.float64, device="cuda")
+    k[..., i], k[..., j] = x * c + y * s, y * c - x * s
+    k[0, :, int(i[-1])] = 400.0 / factor  # the slowest pair of the first row: the scale's value
+    k[0, :, int(j[-1])] = 0.0
+    return k.to(DT[dtype][0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pairs,factor,d,ps,hkv,n", [("half", 1.0, 128, 64, 8, 64), ("neighbour", 0.75, 64, 16, 2, 16),
+                                                      ("half", 0.75, 128, 128, 4, 128), ("neighbour", 1.0, 128, 16, 24, 3)])
+def test_append_keys_between_two_codes(pairs, factor, d, ps, hkv, n, dtype):
+    """Every key of the call at a border, far more than a handful in a block: each code is the exact value's nearest, and
+    two calls give the same bits."""
+    fr = ops.freqs(d, 100.0)
+    old = 5 * ps  # a page of its own
+    pos = torch.arange(old, old + n, device="cuda")
+    k = _border_keys(n, hkv, d, pos, fr, pairs, factor, dtype, 230)
+    h = hkv
+    x = torch.zeros(n, (h + 2 * hkv) * d, dtype=k.dtype, device="cuda")
+    x[:, h * d:(h + hkv) * d] = k.view(n, -1)
+    q_out = torch.empty(n, h, d, dtype=k.dtype, device="cuda")
+    pools = [Pool([old + n], hkv, d, ps, 231) for _ in range(3)]
+    for p in pools:
+        run_append(p, x, q_out, h, [n], [old + n], fr, pairs, dtype, factor)
+    turned = ops.rotate64(k.double(), pos, fr, pairs, factor).transpose(0, 1)
+    page = int(pools[0].table[0, 5])
+    assert bool((pools[0].ks[page] == 1.0).all())
+    have = pools[0].k[page, :, :n].view(torch.float8_e4m3fn).double()
+    want = ops.e4m3_64(turned)
+    _, e = torch.frexp(turned)
+    gap = torch.remainder(turned.abs() * torch.ldexp(torch.ones_like(turned), 4 - e), 1.0) - 0.5
+    sure = gap.abs() > 2.0 ** -38  # past what the float64 forms agree to
+    if dtype == "f32":  # what the pass is for: most are too near for fp32 to tell
+        assert float(((gap.abs() < 2.0 ** -19) & sure).double().mean()) > 0.5
+    wrong = (have != want) & sure
+    assert int(wrong.sum()) == 0, (int(wrong.sum()), wrong.numel())
+    for p in pools[1:]:
+        assert torch.equal(p.k, pools[0].k) and torch.equal(p.ks.nan_to_num(-5.0), pools[0].ks.nan_to_num(-5.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pairs,factor,d,ps,hkv,n", [("half", 1.0, 128, 64, 8, 64), ("neighbour", 0.75, 64, 16, 2, 16)])
+def test_append_rotated_keys_between_two_codes(pairs, factor, d, ps, hkv, n, dtype):
+    """The same keys with the rotated ones asked for, apart and in place: what the cache holds does not depend on it, and
+    both are the rotated keys, rounded once (fp32: three units of the pair's size besides, where fp32 was near enough)."""
+    fr = ops.freqs(d, 100.0)
+    old, h = 5 * ps, hkv
+    pos = torch.arange(old, old + n, device="cuda")
+    k = _border_keys(n, hkv, d, pos, fr, pairs, factor, dtype, 232)
+    x = torch.zeros(n, (h + 2 * hkv) * d, dtype=k.dtype, device="cuda")
+    x[:, h * d:(h + hkv) * d] = k.view(n, -1)
+    q_out, apart, inside = torch.empty(n, h, d, dtype=k.dtype, device="cuda"), torch.empty_like(k), x.clone()
+    pools = [Pool([old + n], hkv, d, ps, 233) for _ in range(3)]
+    run_append(pools[0], x, q_out, h, [n], [old + n], fr, pairs, dtype, factor)
+    run_append(pools[1], x, q_out, h, [n], [old + n], fr, pairs, dtype, factor, k_out=apart)
+    run_append(pools[2], inside, q_out, h, [n], [old + n], fr, pairs, dtype, factor, k_out=inside[:, h * d:])
+    for p in pools[1:]:
+        assert torch.equal(p.k, pools[0].k) and torch.equal(p.v, pools[0].v)
+    assert torch.equal(inside[:, h * d:(h + hkv) * d].reshape_as(apart), apart)
+    exact = ops.rotate64(k.double(), pos, fr, pairs, factor)
+    size = torch.empty_like(exact)
+    i = torch.arange(d // 2, device="cuda")
+    i, j = (i, i + d // 2) if pairs == "half" else (2 * i, 2 * i + 1)
+    size[..., i] = size[..., j] = torch.hypot(k[..., i].double(), k[..., j].double()) * factor
+    assert bool(((apart.double() - exact).abs() <= DT[dtype][2] * exact.abs() + 3 * 2.0 ** -23 * size).all())
+
+
+@pytest.mark.parametrize("dtype,d,ps", [("bf16", 128, 64), ("f32", 64, 16), ("bf16", 64, 128)])
+def test_append_key_codes_are_the_nearest(dtype, d, ps):
+    """Prompts from position 0 on (there the rotation is the identity, and bf16 keys are exact middles one time in 16),
+    half of the frequencies 0 besides: the nearest code wherever the float64 value is further from a middle than fp32's
+    rotation is off (2^-22 of the pair's size, four units), and at exact middles (where it is exact)."""
+    h, hkv, n = 8, 8, 200
+    fr = ops.freqs(d)
+    fr[d // 4:] = 0.0
+    pool = Pool([n], hkv, d, ps, 240)
+    x = (torch.randn(n, (h + 2 * hkv) * d, generator=gen(241), device="cuda") * 1.28).to(DT[dtype][0])
+    q_out = torch.empty(n, h, d, dtype=x.dtype, device="cuda")
+    run_append(pool, x, q_out, h, [n], [n], fr, "half", dtype)
+    k = x.double().view(n, h + 2 * hkv, d)[:, h:h + hkv]
+    turned = ops.rotate64(k, torch.arange(n, device="cuda"), fr, "half", 1.0)
+    size = torch.hypot(k[..., :d // 2], k[..., d // 2:]).repeat(1, 1, 2)
+    for p in range(-(-n // ps)):
+        lo, hi = p * ps, min(n, (p + 1) * ps)
+        page = int(pool.table[0, p])
+        s = pool.ks[page].double()[:, None, None]
+        y, z = (t[lo:hi].transpose(0, 1) / s for t in (turned, size))
+        have = pool.k[page, :, :hi - lo].view(torch.float8_e4m3fn).double()
+        _, e = torch.frexp(y)
+        step = torch.ldexp(torch.ones_like(y), (e - 1).clamp(min=-6) - 3)
+        gap = (torch.remainder(y.abs() / step, 1.0) - 0.5).abs() * step
+        sure = (gap > 2.0 ** -22 * z) | (y == k[lo:hi].transpose(0, 1) / s)
+        assert float(sure.double().mean()) > 0.99
+        assert torch.equal(torch.where(sure, have, 0.0), torch.where(sure, ops.e4m3_64(y), 0.0))
