@@ -344,7 +344,8 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
                                that is negative, shorter than its new tokens or longer than its table row: the
                                sequence is left out (attention: its output rows, up to the given maximum, are
                                zeroed if they can be told) */
-#define DEC_SEQ_TIMEOUT 4   /* a wait inside a kernel ran out (a second; never expected): results are incomplete */
+#define DEC_SEQ_TIMEOUT 4   /* a wait inside a kernel ran out (a second, or the cache's wait_timeout_us; never
+                               expected): results are incomplete, and a workspace can be used again */
 
 #define DEC_ROPE_HALF 0      /* pairs (j, j + rot_dim/2) */
 #define DEC_ROPE_NEIGHBOUR 1 /* pairs (2j, 2j + 1) */
@@ -361,6 +362,7 @@ typedef struct dec_paged_cache {
   float* k_scales; /* [n_pages][n_kv_heads] */
   float* v_scales; /* same */
   int32_t n_pages, page_size, n_kv_heads, head_dim; /* page_size 16, 32, 64 or 128 */
+  uint32_t wait_timeout_us; /* bound on each wait of dec_attention_paged; 0 = 1,000,000 us */
 } dec_paged_cache;
 
 /* The rotation: dims below rot_dim, by angle position * inv_freq[j] for pair j

@@ -468,10 +468,14 @@ struct PagedArgs {
   int table_stride;
   float scale_log2;
   float* part;     // [kBlocks][2] open ends (0: that began before the block, 1: that begins in it): m[8], m'[8], l[8], O[8][D]
-  uint64_t* ready; // [kBlocks][2] `key` once part is written; whoever reads it clears it
-  uint64_t key;    // what `ready` holds then: a number of this process that uninitialised memory does not hold
+  // [kBlocks][2] `key` once part is written, and its reader clears it; gone(key) where the reader's wait ran out first, and
+  // the writer clears it.  So every call leaves none of either behind, and one that was late is not taken for the next call's.
+  uint64_t* ready;
+  uint64_t key;    // a number of this process: uninitialised memory holds neither it nor gone of it
+  uint64_t limit_ns;
   int32_t* status;
 };
+__device__ __forceinline__ uint64_t gone(uint64_t key) { return ~key; }
 
 __device__ __forceinline__ int tiles_of(const PagedArgs& a, int s) {
   const int len = a.lens[s];
@@ -551,6 +555,7 @@ struct PagedShape {
   static constexpr int kSlot = (24 + 8 * D) * 4;    // m[8], m'[8], l[8], O[8][D]
   static constexpr int kRing = kStages * kStage;    // also holds a warp's last open end once its copies are done
   static constexpr int kSmem = kWarps * (kRing + kSlot);
+  static_assert(kThreads >= kBlocks, "a thread for each earlier block's part");
   static_assert(kRing >= kSlot && kSmem <= 227 * 1024 - 24 * 1024, "shared memory");
 };
 
@@ -576,8 +581,10 @@ __device__ __forceinline__ uint64_t load_acquire(const uint64_t* p) {
   asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ void store_release(uint64_t* p, uint64_t v) {
-  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+__device__ __forceinline__ uint64_t exchange(uint64_t* p, uint64_t v) {
+  uint64_t old;
+  asm volatile("atom.acq_rel.gpu.global.exch.b64 %0, [%1], %2;" : "=l"(old) : "l"(p), "l"(v) : "memory");
+  return old;
 }
 
 __device__ __forceinline__ void store4(float* p, float x, float y, float z, float w) {
@@ -1001,12 +1008,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
       } else {
         const int remote = blockIdx.x - first, n = remote + local;
         auto remote_at = [&](int k) { return a.part + (size_t)(2 * (first + k) + (k == 0)) * (24 + 8 * D); };
-        for (int k = tid; k < remote; k += kThreads) {  // the earlier blocks' parts have to be there
-          const uint64_t* r = a.ready + 2 * (first + k) + (k == 0);
+        bool came = true;
+        if (tid < remote) {  // the earlier blocks' parts have to be there
+          uint64_t* r = a.ready + 2 * (first + tid) + (tid == 0);
           const uint64_t t0 = clock_ns();
           while (load_acquire(r) != a.key)
-            if (clock_ns() - t0 > 1000000000ull) {
-              late_s = 1;
+            if (clock_ns() - t0 > a.limit_ns) {
+              came = exchange(r, gone(a.key)) == a.key;
+              if (!came) late_s = 1;
               break;
             }
         }
@@ -1049,11 +1058,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
           put(h, d, x, tot_s[0][h], tot_s[1][h], tot_s[2][h]);
         }
         __syncthreads();
-        for (int k = tid; k < remote; k += kThreads) a.ready[2 * (first + k) + (k == 0)] = 0;  // read: for the next call
+        if (tid < remote && came) a.ready[2 * (first + tid) + (tid == 0)] = 0;  // read: for the next call
         if (tid == 0 && late_s) flag(a.status, DEC_SEQ_TIMEOUT);
       }
       if (!to_end && (shorter ? lane == 0 : tid == 0)) {
-        store_release(a.ready + 2 * blockIdx.x + from_start, a.key);  // behind the barrier above, hence every thread's part
+        uint64_t* r = a.ready + 2 * blockIdx.x + from_start;
+        if (exchange(r, a.key) == gone(a.key)) *r = 0;  // behind the barrier above, hence every thread's part
       }
     }
   }
@@ -1198,7 +1208,8 @@ extern "C" int dec_attention_paged(const dec_paged_cache* cache, int32_t dtype, 
   const size_t flags = kBlocks * 2 * sizeof(uint64_t);
   PagedArgs a{device_cache(cache), q, out, q_stride, out_stride, n_heads / hkv, n_seqs, 31 - __builtin_clz(cache->page_size),
               seq_lens, page_table, table_stride, scale * 1.4426950408889634f,
-              reinterpret_cast<float*>(static_cast<char*>(workspace) + flags), static_cast<uint64_t*>(workspace), key, status};
+              reinterpret_cast<float*>(static_cast<char*>(workspace) + flags), static_cast<uint64_t*>(workspace), key,
+              (cache->wait_timeout_us ? cache->wait_timeout_us : 1000000) * 1000ull, status};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == DEC_BF16)

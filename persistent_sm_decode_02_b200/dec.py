@@ -79,7 +79,7 @@ class dec_tensor(ctypes.Structure):
 class dec_paged_cache(ctypes.Structure):
     _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("wait_timeout_us", ctypes.c_uint32)]
 
 
 class dec_rope(ctypes.Structure):
@@ -387,9 +387,11 @@ class PagedCache:
     operators on it.  Strides are in elements and default to contiguous [rows][heads][head_dim]; scale defaults to
     1/sqrt(head_dim); stream is a cudaStream_t (None: the legacy default stream)."""
 
-    def __init__(self, k_pages, v_pages, k_scales, v_scales, *, n_pages, page_size, n_kv_heads, head_dim):
+    def __init__(self, k_pages, v_pages, k_scales, v_scales, *, n_pages, page_size, n_kv_heads, head_dim,
+                 wait_timeout_us=0):
         self.lib = load_library()
-        self.c = dec_paged_cache(k_pages, v_pages, k_scales, v_scales, n_pages, page_size, n_kv_heads, head_dim)
+        self.c = dec_paged_cache(k_pages, v_pages, k_scales, v_scales, n_pages, page_size, n_kv_heads, head_dim,
+                                 wait_timeout_us)
         self.head_dim, self.kv_row, self.scale = head_dim, n_kv_heads * head_dim, max(1, head_dim) ** -0.5
 
     def append(self, q, k, v, q_out, cu_new, seq_lens, page_table, *, table_stride, n_seqs, n_tokens, max_new, n_heads,

@@ -7,9 +7,10 @@ import math
 import pytest
 import torch
 
+import persistent_sm_decode_02_b200 as pkg
 import test_gpu_operators as ops
 from persistent_sm_decode_02_b200 import dec as D_
-from test_gpu_operators import DT, U, Pool, gen, run_append, run_paged, run_prefill
+from test_gpu_operators import DT, U, Pool, gen, ints, run_append, run_paged, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -115,6 +116,35 @@ def test_paged_small_weights_keep_their_bits(dtype, down):
     tol = DT[dtype][2] * ref.abs() + a * ((2.0 ** -11 if dtype == "bf16" else 2.0 ** -20) + 4 * U * down + 2.0 ** -20 + n * U)
     err = (out.double() - ref).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+def test_paged_workspace_after_a_wait_that_ran_out():
+    """With a limit of a microsecond the join of a long sequence gives up on blocks that end later: flagged, and the next
+    call on the same workspace, on other values, waits for its own blocks' parts.  With the usual limit nothing is flagged."""
+    h, hkv, d, ps, lens = 8, 2, 128, 64, [150_000, 70_000]
+    pool = Pool([ps] * 8, hkv, d, ps, 250).fill([ps] * 8, 251)
+    ids = pool.table[:, 0].clone()
+    pool.width = -(-max(lens) // ps)
+    pool.table = ids[torch.randint(0, 8, (2, pool.width), generator=gen(252), device="cuda")].to(torch.int32)
+    q = torch.randn(2, 2, h, d, generator=gen(253), device="cuda")
+    space = torch.empty(pool.cache().workspace_bytes(2, h), dtype=torch.uint8, device="cuda")
+    want, out, status = torch.empty_like(q), torch.empty_like(q[0]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for i in range(2):
+        run_paged(pool, q[i], want[i], lens, "f32")
+    table, at = pool.table, ints(lens)
+    short = pkg.PagedCache(pool.k.data_ptr(), pool.v.data_ptr(), pool.ks.data_ptr(), pool.vs.data_ptr(), n_pages=pool.n_pages,
+                           page_size=ps, n_kv_heads=hkv, head_dim=d, wait_timeout_us=1)
+    late = 0
+    for _ in range(20):
+        status.zero_()
+        short.attention(q[0].data_ptr(), out.data_ptr(), at.data_ptr(), table.data_ptr(), table_stride=pool.width, n_seqs=2,
+                        n_heads=h, dtype=D_.DEC_F32, workspace=space.data_ptr(), workspace_bytes=space.numel(),
+                        status=status.data_ptr(), stream=ops.stream())
+        late += int(status) == D_.DEC_SEQ_TIMEOUT
+        status.zero_()
+        run_paged(pool, q[1], out, lens, "f32", status=status, space=space)
+        assert int(status) == 0 and torch.equal(out, want[1])
+    assert late > 0
 
 
 # ------------------------------------------------------------------------------------------------ append
