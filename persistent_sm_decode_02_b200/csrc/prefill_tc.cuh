@@ -15,8 +15,9 @@
 // of the unrounded weights, in fp32.
 //
 // An unseen value meets a weight of zero, and zero times NaN or infinity is NaN.  Such values are rare and rows that have
-// met one show it, so it is looked for only in the results: a row that is not finite is computed once more with the keys
-// it sees alone (redo_row).
+// met one show it, so it is looked for only in the results (mend_rows): where a result is not finite although every value
+// that the row sees in that dim is, the row is computed once more with the keys it sees alone.  That takes a warp long
+// where keys are many; the block's other warps wait for it as long as it gets on.
 //
 // What it measures: a causal 8k prompt, 32 heads of 128 on 8, 440-465 us, 1.18-1.25 PFLOP/s (72-76 % of cuBLAS's burst
 // rate); of heads of 64 325 us.  With the softmax left out the MMAs, loads and hand-overs take 395 us: the tensor cores wait
@@ -135,12 +136,17 @@ struct Item {
   int q0, k0, lq, lk, m0, head0, n[2], sound;  // n: steps of each tile; sound: the sequence's ranges are
 };
 
+struct Life {
+  int dead;               // a wait has run out
+  unsigned int progress;  // of rows that are computed once more
+};
+
 struct Bars {  // at most 512 bytes
   uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2], next, drained;
   Item item[2];
   uint4 answer;  // of the request for more work
   uint32_t tmem;
-  int dead;
+  Life life;
 };
 constexpr int kTakers = 10;  // warps that read an item
 
@@ -155,28 +161,34 @@ __device__ __forceinline__ bool elect() {
 
 __device__ __forceinline__ uint64_t now_ns() { return dec::globaltimer(); }
 
-// Waits for a phase of an mbarrier, a second at most (another warp's failure ends it too, where `dead` is given).
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  const uint64_t t0 = now_ns();
+// Waits for a phase of an mbarrier, a second without progress at most (another warp's failure ends it too, where `life` is
+// given).
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile Life* life) {
+  uint64_t t0 = now_ns();
+  unsigned int progress = life ? life->progress : 0;
   for (;;) {
     if (dec::mbar_try_wait(bar, parity)) return true;
-    if (dead && *dead) return false;
+    if (life && life->dead) return false;
     if (now_ns() - t0 > 1000000000ull) {
-      if (dead) *dead = 1;
-      return false;
+      if (!life) return false;
+      if (life->progress == progress) {
+        life->dead = 1;
+        return false;
+      }
+      t0 = now_ns(), progress = life->progress;
     }
   }
 }
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Life* life) {
   for (int i = 0; i < 16; ++i)
     if (dec::mbar_try_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, dead);
+  return wait_slow(bar, parity, life);
 }
 // The same for a whole warp, whose lanes stay together.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* dead) {
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Life* life) {
   for (int i = 0; i < 16; ++i)
     if (__all_sync(0xffffffffu, dec::mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, wait_slow(bar, parity, dead));
+  return __all_sync(0xffffffffu, wait_slow(bar, parity, life));
 }
 
 // More work: the number of a block of this launch that has not begun and now never will, in place of which this block
@@ -294,9 +306,10 @@ __device__ __forceinline__ F2 exp2_poly(F2 v) {
 
 // One row over the `n` keys it sees, on a warp: lanes take keys for the scores and dims for the values.
 template <int D>
-__device__ __forceinline__ void redo_row(const PrefillArgs& a, const __nv_bfloat16* q, const __nv_bfloat16* k,
-                                      const __nv_bfloat16* v, __nv_bfloat16* out, int n) {
+__device__ __forceinline__ void redo_row(const PrefillArgs& a, Life* life, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                         const __nv_bfloat16* v, __nv_bfloat16* out, int n) {
   constexpr int kD = D / 32;
+  using Values = std::conditional_t<D == 128, uint2, uint32_t>;  // a lane's dims
   const int lane = threadIdx.x & 31;
   float m = -INFINITY, l = 0.f, o[kD] = {};
   for (int t0 = 0; t0 < n; t0 += 32) {
@@ -305,29 +318,108 @@ __device__ __forceinline__ void redo_row(const PrefillArgs& a, const __nv_bfloat
     if (t < n) {
       s = 0.f;
 #pragma unroll 1
-      for (int d = 0; d < D; d += 8) {
-        Vec8<__nv_bfloat16> x, y;
-        float u[8], w[8];
-        x.load(q + d);
-        y.load(k + t * a.ks + d);
-        x.get(u);
-        y.get(w);
-        for (int i = 0; i < 8; ++i) s = fmaf(u[i], w[i], s);
+      for (int d = 0; d < D; d += 32) {
+        Vec8<__nv_bfloat16> x[4], y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c].load(k + t * a.ks + d + 8 * c), x[c].load(q + d + 8 * c);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float u[8], w[8];
+          x[c].get(u);
+          y[c].get(w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s = fmaf(u[i], w[i], s);
+        }
       }
       s *= a.scale_log2;
     }
     const float mn = fmaxf(m, warp_max(s)), base = mn == -INFINITY ? 0.f : mn, f = exp2f(m - base);
     const float p = t < n ? exp2f(s - base) : 0.f;
     l = l * f + warp_sum(p);
+#pragma unroll
     for (int i = 0; i < kD; ++i) o[i] *= f;
 #pragma unroll 1
-    for (int j = 0; j < 32 && t0 + j < n; ++j) {
-      const float pj = __shfl_sync(0xffffffffu, p, j);
-      for (int i = 0; i < kD; ++i) o[i] = fmaf(pj, __bfloat162float(v[(t0 + j) * a.vs + lane * kD + i]), o[i]);
+    for (int j0 = 0; j0 < 32 && t0 + j0 < n; j0 += 8) {
+      Values x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (t0 + j0 + j < n) x[j] = *reinterpret_cast<const Values*>(v + (t0 + j0 + j) * a.vs + lane * kD);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float pj = __shfl_sync(0xffffffffu, p, j0 + j);
+        if (t0 + j0 + j < n) {
+          const __nv_bfloat16* y = reinterpret_cast<const __nv_bfloat16*>(&x[j]);
+#pragma unroll
+          for (int i = 0; i < kD; ++i) o[i] = fmaf(pj, __bfloat162float(y[i]), o[i]);
+        }
+      }
     }
     m = mn;
+    if (lane == 0) atomicAdd(&life->progress, 1u);
   }
+#pragma unroll
   for (int i = 0; i < kD; ++i) out[lane * kD + i] = __float2bfloat16_rn(o[i] / l);
+}
+
+// Which of eight values are not finite.
+__device__ __forceinline__ uint32_t not_finite(const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r |= (w[i] & 0x7F80u) == 0x7F80u ? 1u << 2 * i : 0u;
+    r |= (w[i] & 0x7F800000u) == 0x7F800000u ? 2u << 2 * i : 0u;
+  }
+  return r;
+}
+
+// Results of a warp's rows (lane's row: `end` keys are seen) that are not finite, in the rows of `rows`: they stand where the
+// row sees a value in that dim that is not finite either; else the row is computed once more.  q and out: the first lane's row.
+template <int D>
+__device__ __forceinline__ void mend_rows(const PrefillArgs& a, Life* life, uint32_t rows, int end, const __nv_bfloat16* q,
+                                          const __nv_bfloat16* k, const __nv_bfloat16* v, __nv_bfloat16* out) {
+  constexpr int kLanes = D / 8, kKeys = 32 / kLanes, kAhead = 8;  // of a key; keys of a load; loads under way
+  const int lane = threadIdx.x & 31, dim = lane % kLanes * 8, sub = lane / kLanes;
+  const int top = __shfl_sync(0xffffffffu, end, 31 - __clz(rows));  // (later rows see no fewer)
+  uint32_t open = 0;  // dims in question for which no such value is found yet
+  for (uint32_t left = rows; left; left &= left - 1)
+    open |= not_finite(*reinterpret_cast<const uint4*>(out + (__ffs(left) - 1) * a.os + dim));
+  int first[8];  // the first key with such a value
+#pragma unroll
+  for (int i = 0; i < 8; ++i) first[i] = 0x7FFFFFFF;
+  for (int t0 = 0; t0 < top && __any_sync(0xffffffffu, open != 0); t0 += kKeys * kAhead) {
+    uint4 x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = t0 + u * kKeys + sub;
+      x[u] = t < top ? *reinterpret_cast<const uint4*>(v + t * a.vs + dim) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const uint32_t found = not_finite(x[u]) & open;
+      if (found) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (found >> i & 1) first[i] = t0 + u * kKeys + sub;
+        open &= ~found;
+      }
+    }
+#pragma unroll
+    for (int w = kLanes; w < 32; w <<= 1) open &= __shfl_xor_sync(0xffffffffu, open, w);
+    if (lane == 0) atomicAdd(&life->progress, 1u);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int w = kLanes; w < 32; w <<= 1) first[i] = min(first[i], __shfl_xor_sync(0xffffffffu, first[i], w));
+  for (uint32_t left = rows; left; left &= left - 1) {
+    const int r = __ffs(left) - 1, n = __shfl_sync(0xffffffffu, end, r);
+    const uint32_t bad = not_finite(*reinterpret_cast<const uint4*>(out + r * a.os + dim));
+    bool again = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) again |= (bad >> i & 1) && first[i] >= n;
+    if (__any_sync(0xffffffffu, again)) redo_row<D>(a, life, q + r * a.qs, k, v, out + r * a.os, n);
+  }
 }
 
 template <int D, bool kPacked>
@@ -380,7 +472,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
     }
     dec::mbar_init(&b.next, 1);
     dec::mbar_init(&b.drained, 1);
-    b.dead = 0;
+    b.life.dead = 0, b.life.progress = 0;
     dec::fence_mbar_init();
   }
   if (warp == 8) {
@@ -400,7 +492,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
       w = only;
       return round == 0;
     }
-    ok = ok && wait_warp(&b.item_full[round & 1], round >> 1 & 1, &b.dead);
+    ok = ok && wait_warp(&b.item_full[round & 1], round >> 1 & 1, &b.life);
     if (!ok) return false;
     w = b.item[round & 1];
     return w.m0 >= 0;
@@ -428,7 +520,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
       }
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++step) {
-        ok = wait_warp(&b.s_full[i], step & 1, &b.dead);
+        ok = wait_warp(&b.s_full[i], step & 1, &b.life);
         if (!ok) break;
         dec::tc_fence_after();
         uint32_t x[kN / 32][32];
@@ -504,7 +596,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
       if (!ok) break;
       // ---- results
       if (n > 0) {
-        ok = wait_warp(&b.o_full[i], written++ & 1, &b.dead);
+        ok = wait_warp(&b.o_full[i], written++ & 1, &b.life);
         if (!ok) break;
         dec::tc_fence_after();
       }
@@ -513,11 +605,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
       leave(round);
       const int row = w.m0 + i * mstep + (tid & 127), head = w.head0 + (pair ? i : 0);
       const bool live = row < w.lq;
-      // No score above -infinity.  (The sum does not tell: the polynomial gives such a score 2^-126.)
-      const bool none = m == -INFINITY || l == 0.f;
-      const float inv = none ? 0.f : 1.f / l;
+      // No softmax, hence NaN: every score is -infinity (the maximum tells; the polynomial gives such a score 2^-126), or
+      // one is +infinity or NaN (the sum of sound weights is below 2^8 a key; the polynomial gives a NaN 2^127)
+      const bool none = end <= 0, lost = m == -INFINITY || !(l > 0.f && l < 1e30f);
+      const float inv = lost ? NAN : 1.f / l;
       bf16* op = static_cast<bf16*>(a.out) + ((int64_t)w.q0 + row) * a.os + (int64_t)head * D;
-      bool bad = none;  // where it sees any, NaN
+      bool bad = false;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -540,17 +633,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
         }
       }
       dec::tc_fence_before();  // O is read: the next item's first P lets it be written
-      uint32_t again = __ballot_sync(0xffffffffu, bad && live && end > 0);
-      while (again) {
-        const int k = __ffs(again) - 1;
-        again &= again - 1;
-        const int64_t rw = __shfl_sync(0xffffffffu, row, k);
-        __syncwarp();  // the row's first result is written
-        redo_row<D>(a, static_cast<const bf16*>(a.q) + (w.q0 + rw) * a.qs + (int64_t)head * D,
-                    static_cast<const bf16*>(a.k) + (int64_t)w.k0 * a.ks + (int64_t)(head / a.gs) * D,
-                    static_cast<const bf16*>(a.v) + (int64_t)w.k0 * a.vs + (int64_t)(head / a.gs) * D,
-                    static_cast<bf16*>(a.out) + (w.q0 + rw) * a.os + (int64_t)head * D,
-                    __shfl_sync(0xffffffffu, end, k));
+      const uint32_t again = __ballot_sync(0xffffffffu, bad && live && !none && !lost);
+      if (again) {
+        __syncwarp();  // the rows' first results are written
+        const int64_t r0 = (int64_t)w.q0 + w.m0 + i * mstep + (tid & 96);  // the first lane's row
+        mend_rows<D>(a, &b.life, again, end, static_cast<const bf16*>(a.q) + r0 * a.qs + (int64_t)head * D,
+                     static_cast<const bf16*>(a.k) + (int64_t)w.k0 * a.ks + (int64_t)(head / a.gs) * D,
+                     static_cast<const bf16*>(a.v) + (int64_t)w.k0 * a.vs + (int64_t)(head / a.gs) * D,
+                     static_cast<bf16*>(a.out) + r0 * a.os + (int64_t)head * D);
       }
     }
     if (!ok && lane == 0) flag(a.status, DEC_SEQ_TIMEOUT);
@@ -566,7 +656,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
         leave(round);
         const int n_max = max(w.n[0], w.n[1]);
         if (n_max > 0 && elect()) {
-          ok = n_q == 0 || wait(&b.q_empty, (n_q - 1) & 1, &b.dead);
+          ok = n_q == 0 || wait(&b.q_empty, (n_q - 1) & 1, &b.life);
           if (ok) {
             const int tiles_q = w.n[1] > 0 ? 2 : 1;
             mbar_arrive_expect_tx(&b.q_full, tiles_q * Sh::kQ);
@@ -578,7 +668,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
           }
           for (int j = 0; j < 2 * n_max && ok; ++j) {
             const int slot = issued % Sh::kStages, turn = issued / Sh::kStages;
-            ok = turn == 0 || wait(&b.kv_empty[slot], (turn - 1) & 1, &b.dead);
+            ok = turn == 0 || wait(&b.kv_empty[slot], (turn - 1) & 1, &b.life);
             if (!ok) break;
             mbar_arrive_expect_tx(&b.kv_full[slot], Sh::kTile);
             for (int c = 0; c < kSlabs; ++c)
@@ -605,9 +695,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
         leave(round);
         const int n0 = __shfl_sync(0xffffffffu, w.n[0], 0), n1 = __shfl_sync(0xffffffffu, w.n[1], 0), n_max = max(n0, n1);
         if (n_max == 0) continue;
-        ok = wait_warp(&b.q_full, n_q++ & 1, &b.dead);
+        ok = wait_warp(&b.q_full, n_q++ & 1, &b.life);
         auto full = [&](uint32_t x) {  // the x-th load's place in the ring, in units of 16 bytes
-          ok = ok && wait_warp(&b.kv_full[x % Sh::kStages], (x / Sh::kStages) & 1, &b.dead);
+          ok = ok && wait_warp(&b.kv_full[x % Sh::kStages], (x / Sh::kStages) & 1, &b.life);
           return x % Sh::kStages * (Sh::kTile >> 4);
         };
         auto release = [&](int x) {  // the item's x-th load's slot, if it will be filled again
@@ -651,7 +741,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
           for (int i = 0; i < 2; ++i) {
             const int n = i ? n1 : n0;
             if (j >= n) continue;
-            ok = ok && wait_warp(&b.p_full[i], step[i]++ & 1, &b.dead);
+            ok = ok && wait_warp(&b.p_full[i], step[i]++ & 1, &b.life);
             if (!ok) break;
             dec::tc_fence_after();
             values(i, j, n, vt);
@@ -679,7 +769,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
         Item w;
         const bool some = at >= 0 && item_at(at, w);
         if (some || at < 0) {
-          if (round > 1) ok = wait_warp(&b.item_empty[round & 1], (round >> 1) - 1 & 1, &b.dead);
+          if (round > 1) ok = wait_warp(&b.item_empty[round & 1], (round >> 1) - 1 & 1, &b.life);
           if (at < 0) w.m0 = -1;
           if (ok && lane == 0) {
             b.item[round & 1] = w;
@@ -689,7 +779,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
         }
         if (at < 0) break;
         if (!__all_sync(0xffffffffu, wait_slow(&b.next, asked++ & 1, nullptr))) {  // an answer may not be under way either
-          b.dead = 1;
+          b.life.dead = 1;
           break;
         }
         at = answer_of(&b.answer);

@@ -39,6 +39,78 @@ def test_prefill_rows_whose_every_score_is_minus_infinity(kind, d, causal, dtype
     assert torch.equal(out[~bad], clean[~bad])
 
 
+@pytest.mark.parametrize("d,n", [(64, 5000), (128, 5000), (128, 30000)])
+@pytest.mark.parametrize("what", ["value", "value_inf", "key", "late"])
+def test_prefill_bf16_values_that_are_not_finite_in_a_long_prompt(what, d, n):
+    """A NaN that nearly every row of a long prompt sees shows in its dim (value) or row (key) there; every other result of
+    that prompt, and the prompt beside it, have the bits they have without it, and no wait runs out meanwhile."""
+    h, hkv, lens = 4, 2, [n, 700]
+    q, k, v = ops.prefill_inputs(h, hkv, d, sum(lens), sum(lens), "bf16", 260)
+    clean, out = torch.empty_like(q), torch.empty_like(q)
+    run_prefill(q, k, v, clean, lens, lens, "bf16")
+    at = n // 2 + 3 if what == "late" else 0
+    if what == "key":
+        k[at, 0, 9] = math.nan
+    else:
+        v[at, 0, 9] = math.inf if what == "value_inf" else math.nan
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    run_prefill(q, k, v, out, lens, lens, "bf16", status=status)
+    assert int(status) == 0
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    if what == "key":
+        bad[at:n, :2] = True
+    else:
+        bad[at:n, :2, 9] = True
+    if what == "value_inf":  # the weight of a far key may round to zero
+        assert not bool(torch.isfinite(out[bad]).any()) and bool((out[at, :2, 9] == math.inf).all())
+    else:
+        assert bool(torch.isnan(out[bad]).all())
+    same = ~bad
+    tile = slice(at - at % 128, at)  # rows that share a step with it and do not see it are computed once more
+    same[tile, :2] = False
+    assert torch.equal(out[same], clean[same])
+    if tile.stop > tile.start:
+        k, v = k[:at], v[:at]
+        seen = torch.arange(at, device="cuda")[None, :] <= torch.arange(tile.start, tile.stop, device="cuda")[:, None]
+        ref, a, s = ops.attend64(*(t.double().transpose(0, 1) for t in (q[tile, :2], k[:, :1], v[:, :1])), d ** -0.5, seen)
+        tol = ops.attend_tol(ref, a, s, at, d, "bf16", 2.0 ** -8)
+        assert bool(((out[tile, :2].double().transpose(0, 1) - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_bf16_some_values_seen_some_not(d):
+    """NaN in dim 3 of the first key, which every row sees, in dim 7 of a key inside the last tile, and in all dims of the
+    next prompt's first keys: dim 3 is NaN, dim 7 from that key's row on, and all else is finite and right."""
+    h, hkv, lens, at = 2, 1, [1000, 60], 950
+    q, k, v = ops.prefill_inputs(h, hkv, d, sum(lens), sum(lens), "bf16", 261)
+    v[0, 0, 3] = v[at, 0, 7] = math.nan
+    v[1000:1003] = math.nan
+    out = torch.empty_like(q)
+    run_prefill(q, k, v, out, lens, lens, "bf16")
+    assert bool(torch.isnan(out[:1000, :, 3]).all()) and bool(torch.isnan(out[at:1000, :, 7]).all())
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[:1000, :, 3] = bad[at:1000, :, 7] = True
+    v[0, 0, 3] = v[at, 0, 7] = 0.0
+    n = 1000
+    seen = torch.arange(n, device="cuda")[None, :] <= torch.arange(n, device="cuda")[:, None]
+    ref, a, s = ops.attend64(*(t[:n].double().transpose(0, 1) for t in (q, k, v)), d ** -0.5, seen)
+    ok = (out[:n].double().transpose(0, 1) - ref).abs() <= ops.attend_tol(ref, a, s, n, d, "bf16", 2.0 ** -8)
+    assert bool((ok | bad[:n].transpose(0, 1)).all())
+    assert bool(torch.isnan(out[1000:]).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_bf16_largest_values(d):
+    """Values of 1e36: weights count up to 2^8 of the row's largest, and their sum passes fp32's range; the result does not."""
+    h, hkv, n = 2, 1, 300
+    q, k, v = ops.prefill_inputs(h, hkv, d, n, n, "bf16", 262)
+    v = (v.float().abs().clamp(0.5, 1.0) * 1e36).bfloat16()
+    k[:200] *= 0.1
+    out = torch.empty_like(q)
+    run_prefill(q, k, v, out, [n], [n], "bf16")
+    ops.check_prefill(q, k, v, out, [n], [n], "bf16")
+
+
 # ------------------------------------------------------------------------------------------------ paged attention
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,first", [(40, 16), (40, 17), (33, 32), (600, 100), (600, 590), (9000, 4000), (40, 40), (9000, 9000)])
