@@ -14,10 +14,12 @@
 // P is rounded to bf16 (2^-9 of each weight, of the same size as V's own rounding and the result's); its sum is
 // of the unrounded weights, in fp32.
 //
-// An unseen value meets a weight of zero, and zero times NaN or infinity is NaN.  Such values are rare and rows that have
-// met one show it, so it is looked for only in the results (mend_rows): where a result is not finite although every value
-// that the row sees in that dim is, the row is computed once more with the keys it sees alone.  That takes a warp long
-// where keys are many; the block's other warps wait for it as long as it gets on.
+// An unseen value meets a weight of zero, and zero times NaN or infinity is NaN.  Values behind a sequence's last key (another
+// sequence's, or nobody's) are zeroed in shared memory before P V of the step that holds it.  (To cut that P V short at the
+// 16 keys that hold it and zero up to 15 rows instead: 2-4 % slower, for the branch in every step.)  Among a sequence's own
+// keys such values are rare and rows that have met one show it, so it is looked for only in the results (mend_rows): where a
+// result is not finite although every value that the row sees in that dim is, the row is computed once more with the keys it
+// sees alone.  That takes a warp long where keys are many; the block's other warps wait for it as long as it gets on.
 //
 // What it measures: a causal 8k prompt, 32 heads of 128 on 8, 440-465 us, 1.18-1.25 PFLOP/s (72-76 % of cuBLAS's burst
 // rate); of heads of 64 325 us.  With the softmax left out the MMAs, loads and hand-overs take 395 us: the tensor cores wait
@@ -694,7 +696,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
         if (!take(round, w)) break;
         leave(round);
         const int n0 = __shfl_sync(0xffffffffu, w.n[0], 0), n1 = __shfl_sync(0xffffffffu, w.n[1], 0), n_max = max(n0, n1);
+        const int lk = __shfl_sync(0xffffffffu, w.lk, 0);
         if (n_max == 0) continue;
+        const int last = lk < n_max * kN ? n_max - 1 : -1;  // the step that holds the last key and others behind it
         ok = wait_warp(&b.q_full, n_q++ & 1, &b.life);
         auto full = [&](uint32_t x) {  // the x-th load's place in the ring, in units of 16 bytes
           ok = ok && wait_warp(&b.kv_full[x % Sh::kStages], (x / Sh::kStages) & 1, &b.life);
@@ -737,6 +741,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
         for (int j = 0; j < n_max && ok; ++j) {
           const uint32_t vt = full(taken + 2 * j + 1);
           if (j + 1 < n_max) kt = full(taken + 2 * j + 2);
+          if (j == last && ok) {
+            const int keys = lk - j * kN, rows = kN - keys;
+            uint8_t* to = ring + (taken + 2 * j + 1) % Sh::kStages * Sh::kTile + keys * kRow;
+            for (int e = lane; e < rows * 8 * kSlabs; e += 32)
+              *reinterpret_cast<uint4*>(to + e / (rows * 8) * kSlab + e % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
+            dec::fence_async_smem();
+            __syncwarp();
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int n = i ? n1 : n0;

@@ -10,7 +10,7 @@ import torch
 import persistent_sm_decode_02_b200 as pkg
 import test_gpu_operators as ops
 from persistent_sm_decode_02_b200 import dec as D_
-from test_gpu_operators import DT, U, Pool, gen, ints, run_append, run_paged, run_prefill
+from test_gpu_operators import DT, U, Pool, gen, ints, offsets, run_append, run_paged, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -75,6 +75,25 @@ def test_prefill_bf16_values_that_are_not_finite_in_a_long_prompt(what, d, n):
         ref, a, s = ops.attend64(*(t.double().transpose(0, 1) for t in (q[tile, :2], k[:, :1], v[:, :1])), d ** -0.5, seen)
         tol = ops.attend_tol(ref, a, s, at, d, "bf16", 2.0 ** -8)
         assert bool(((out[tile, :2].double().transpose(0, 1) - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("h,hkv,d", [(4, 2, 64), (3, 1, 64), (4, 2, 128), (3, 3, 128)])
+def test_prefill_bf16_bits_do_not_depend_on_what_lies_around(h, hkv, d, causal):
+    """NaN and infinities in every key and value of the other prompts, and behind the last: the same bits."""
+    lq, lk = [700, 77, 128, 333, 15, 250], [700, 77, 128, 400, 16, 257]
+    q, k, v = ops.prefill_inputs(h, hkv, d, sum(lq), sum(lk) + 40, "bf16", 263)
+    clean = torch.empty_like(q)
+    run_prefill(q, k, v, clean, lq, lk, "bf16", causal, n_k=sum(lk) + 40)
+    ops.check_prefill(q, k, v, clean, lq, lk, "bf16", causal)
+    for b in range(len(lq)):
+        q0, k0 = offsets(lq)[b], offsets(lk)[b]
+        kk, vv = torch.full_like(k, math.nan), torch.full_like(v, math.nan)
+        vv[::3] = math.inf
+        kk[k0:k0 + lk[b]], vv[k0:k0 + lk[b]] = k[k0:k0 + lk[b]], v[k0:k0 + lk[b]]
+        out = torch.empty_like(q)
+        run_prefill(q, kk, vv, out, lq, lk, "bf16", causal, n_k=sum(lk) + 40)
+        assert torch.equal(out[q0:q0 + lq[b]], clean[q0:q0 + lq[b]]), b
 
 
 @pytest.mark.parametrize("d", [64, 128])
