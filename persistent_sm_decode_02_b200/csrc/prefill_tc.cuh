@@ -6,6 +6,8 @@
 // Warps 0-3 and 4-7 are the tiles' softmax, a thread a row; warp 8 issues every MMA; warp 9 every TMA load; warp 10 finds work.
 //   TMEM: S0 | S1 (kN columns each, P in the first kN / 2) | O0 | O1 (D columns each)
 //   shared memory: Q, and a ring of K and V tiles, rows of 128 bytes in the 128-byte swizzle
+// A score is taken off its row's maximum by one fma, which is off by half an ulp of the maximum: from 2^26 on (kHuge) that is
+// no longer small beside the weights' range, and a warp that met such a maximum computes its rows once more (redo_row).
 // The tiles alternate: while one tile's softmax runs, the tensor cores do the other's P V and next Q K^T.
 // One thread's MMAs complete in the order they were issued.  So S_i(j + 1), issued behind P V_i(j), may overwrite P_i(j),
 // and once it has arrived O_i is at rest until the tile's next P: a softmax thread may rescale its row of O there.  It
@@ -112,6 +114,8 @@ constexpr int kM = 128;
 constexpr int kPoly = 2;
 constexpr float kC0 = 0x1.fff692p-1f, kC1 = 0x1.62f31ap-1f, kC2 = 0x1.f0de1ap-3f, kC3 = 0x1.c3f75ep-5f;
 
+constexpr float kHuge = 0x1p26f;
+
 // Heads of 128: S and O of two tiles with steps of 128 keys fill an SM's TMEM, one block has the SM to itself, and its
 // softmax threads keep a row of S in registers that they take over from the last warpgroup.  The block stays: warp 10 asks
 // for the work of blocks that have not begun, and while the softmax warps write one pair of tiles the next one's loads and
@@ -149,6 +153,7 @@ struct Bars {  // at most 512 bytes
   uint4 answer;  // of the request for more work
   uint32_t tmem;
   Life life;
+  int huge[8];  // of a softmax warp: a maximum of an item's rows was
 };
 constexpr int kTakers = 10;  // warps that read an item
 
@@ -376,15 +381,16 @@ __device__ __forceinline__ uint32_t not_finite(const uint4& x) {
 }
 
 // Results of a warp's rows (lane's row: `end` keys are seen) that are not finite, in the rows of `rows`: they stand where the
-// row sees a value in that dim that is not finite either; else the row is computed once more.  q and out: the first lane's row.
+// row sees a value in that dim that is not finite either; else the row is computed once more (`all`: in any case).  q and
+// out: the first lane's row.
 template <int D>
-__device__ __forceinline__ void mend_rows(const PrefillArgs& a, Life* life, uint32_t rows, int end, const __nv_bfloat16* q,
+__device__ __forceinline__ void mend_rows(const PrefillArgs& a, Life* life, uint32_t rows, bool all, int end, const __nv_bfloat16* q,
                                           const __nv_bfloat16* k, const __nv_bfloat16* v, __nv_bfloat16* out) {
   constexpr int kLanes = D / 8, kKeys = 32 / kLanes, kAhead = 8;  // of a key; keys of a load; loads under way
   const int lane = threadIdx.x & 31, dim = lane % kLanes * 8, sub = lane / kLanes;
   const int top = __shfl_sync(0xffffffffu, end, 31 - __clz(rows));  // (later rows see no fewer)
   uint32_t open = 0;  // dims in question for which no such value is found yet
-  for (uint32_t left = rows; left; left &= left - 1)
+  for (uint32_t left = all ? 0 : rows; left; left &= left - 1)
     open |= not_finite(*reinterpret_cast<const uint4*>(out + (__ffs(left) - 1) * a.os + dim));
   int first[8];  // the first key with such a value
 #pragma unroll
@@ -417,7 +423,7 @@ __device__ __forceinline__ void mend_rows(const PrefillArgs& a, Life* life, uint
   for (uint32_t left = rows; left; left &= left - 1) {
     const int r = __ffs(left) - 1, n = __shfl_sync(0xffffffffu, end, r);
     const uint32_t bad = not_finite(*reinterpret_cast<const uint4*>(out + r * a.os + dim));
-    bool again = false;
+    bool again = all;
 #pragma unroll
     for (int i = 0; i < 8; ++i) again |= (bad >> i & 1) && first[i] >= n;
     if (__any_sync(0xffffffffu, again)) redo_row<D>(a, life, q + r * a.qs, k, v, out + r * a.os, n);
@@ -475,6 +481,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
     dec::mbar_init(&b.next, 1);
     dec::mbar_init(&b.drained, 1);
     b.life.dead = 0, b.life.progress = 0;
+    for (int i = 0; i < 8; ++i) b.huge[i] = 0;
     dec::fence_mbar_init();
   }
   if (warp == 8) {
@@ -548,6 +555,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
           const float f = grow ? dec::ex2_approx((m - mn) * sl) : 1.f;
           l *= f;
           m = mn;
+          if (grow && fabsf(m) * sl >= kHuge && m < INFINITY) b.huge[warp] = 1;
           if (j > 0) {
             // S(j) was issued behind P V of the step before: O is at rest until this step's P
 #pragma unroll 1
@@ -607,9 +615,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
       leave(round);
       const int row = w.m0 + i * mstep + (tid & 127), head = w.head0 + (pair ? i : 0);
       const bool live = row < w.lq;
+      __syncwarp();
+      const bool huge = *static_cast<volatile int*>(&b.huge[warp]);
       // No softmax, hence NaN: every score is -infinity (the maximum tells; the polynomial gives such a score 2^-126), or
-      // one is +infinity or NaN (the sum of sound weights is below 2^8 a key; the polynomial gives a NaN 2^127)
-      const bool none = end <= 0, lost = m == -INFINITY || !(l > 0.f && l < 1e30f);
+      // one is +infinity or NaN (the sum of sound weights is below 2^12 a key; the polynomial gives a NaN 2^127)
+      const bool none = end <= 0, lost = fabsf(m) == INFINITY || (!huge && !(l > 0.f && l < 1e30f));
       const float inv = lost ? NAN : 1.f / l;
       bf16* op = static_cast<bf16*>(a.out) + ((int64_t)w.q0 + row) * a.os + (int64_t)head * D;
       bool bad = false;
@@ -635,11 +645,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
         }
       }
       dec::tc_fence_before();  // O is read: the next item's first P lets it be written
-      const uint32_t again = __ballot_sync(0xffffffffu, bad && live && !none && !lost);
+      const uint32_t again = __ballot_sync(0xffffffffu, (bad || huge) && live && !none && !lost);
+      if (huge && lane == 0) b.huge[warp] = 0;
       if (again) {
         __syncwarp();  // the rows' first results are written
         const int64_t r0 = (int64_t)w.q0 + w.m0 + i * mstep + (tid & 96);  // the first lane's row
-        mend_rows<D>(a, &b.life, again, end, static_cast<const bf16*>(a.q) + r0 * a.qs + (int64_t)head * D,
+        mend_rows<D>(a, &b.life, again, huge, end, static_cast<const bf16*>(a.q) + r0 * a.qs + (int64_t)head * D,
                      static_cast<const bf16*>(a.k) + (int64_t)w.k0 * a.ks + (int64_t)(head / a.gs) * D,
                      static_cast<const bf16*>(a.v) + (int64_t)w.k0 * a.vs + (int64_t)(head / a.gs) * D,
                      static_cast<bf16*>(a.out) + r0 * a.os + (int64_t)head * D);
@@ -744,8 +755,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kBlocks)
           if (j == last && ok) {
             const int keys = lk - j * kN, rows = kN - keys;
             uint8_t* to = ring + (taken + 2 * j + 1) % Sh::kStages * Sh::kTile + keys * kRow;
-            for (int e = lane; e < rows * 8 * kSlabs; e += 32)
-              *reinterpret_cast<uint4*>(to + e / (rows * 8) * kSlab + e % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int e = lane * 16; e < rows * kRow; e += 512)
+#pragma unroll
+              for (int c = 0; c < kSlabs; ++c) *reinterpret_cast<uint4*>(to + c * kSlab + e) = make_uint4(0, 0, 0, 0);
             dec::fence_async_smem();
             __syncwarp();
           }

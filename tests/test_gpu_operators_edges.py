@@ -130,6 +130,45 @@ def test_prefill_bf16_largest_values(d):
     ops.check_prefill(q, k, v, out, [n], [n], "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e6, 1e8, 1e10, 1e15])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_scores_of_any_finite_size(d, size, dtype):
+    """Keys along one direction: the longest seen has all the weight, its value is the result (rounded once; sums of one
+    weight of any size and zeros are exact to 2^-20 and, on the tensor cores, the weight's rounding)."""
+    h, hkv, n = 4, 2, 300
+    g = gen(270)
+    sign = torch.randint(0, 2, (d,), generator=g, device="cuda") * 2.0 - 1.0
+    length = torch.full((n,), 0.25, device="cuda")
+    length[1::3] = 0.5
+    best = [0, 40, 130, 200]  # 1, 2, 4, 8
+    for i, t in enumerate(best):
+        length[t] = 2.0 ** i
+    q = (size * sign).expand(n, h, d).to(DT[dtype][0]).contiguous()
+    k = (length[:, None, None] * sign).expand(n, hkv, d).to(DT[dtype][0]).contiguous()
+    v = torch.randn(n, hkv, d, generator=g, device="cuda").to(DT[dtype][0])
+    out = torch.empty_like(q)
+    run_prefill(q, k, v, out, [n], [n], dtype)
+    of = torch.tensor([max(t for t in best if t <= i) for i in range(n)], device="cuda")
+    ref = v[of].double().repeat_interleave(h // hkv, 1)
+    tol = (DT[dtype][2] + 2.0 ** -20 + (2.0 ** -8 if dtype == "bf16" else 0.0)) * ref.abs()
+    assert bool(((out.double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("low", [-1e9, -1e15, -1e30])
+def test_prefill_first_scores_far_below_the_others(low, d, dtype):
+    """A first step of scores of enormous size and ordinary ones behind it: these alone have weight."""
+    h, hkv, n, first = 4, 2, 400, 130
+    q, k, v = ops.prefill_inputs(h, hkv, d, n, n, dtype, 274)
+    q = q.abs() + 0.5
+    k[:first] = low
+    out = torch.empty_like(q)
+    run_prefill(q, k, v, out, [n], [n], dtype)
+    ops.check_prefill(q[first:], k[first:], v[first:], out[first:], [n - first], [n - first], dtype)
+
+
 # ------------------------------------------------------------------------------------------------ paged attention
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,first", [(40, 16), (40, 17), (33, 32), (600, 100), (600, 590), (9000, 4000), (40, 40), (9000, 9000)])
