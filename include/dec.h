@@ -406,7 +406,7 @@ int dec_attention_paged_workspace(const dec_paged_cache* cache, int32_t n_seqs, 
 
 /* Attention of one query token a sequence over its seq_lens[s] cached positions:
  * out[s][h] = softmax_t(scale * q[s][h] . K[t]) V[t], t < seq_lens[s]; zeros for an
- * empty sequence.  What the pages hold behind the length is never used.
+ * empty sequence.  What the pages hold behind the length is never used.  Finite scores may be as large as 10^8.
  *   q, out     [n_seqs] rows, 16-byte aligned, strides multiples of 16 bytes; out does not overlap q
  *   workspace  dec_attention_paged_workspace bytes, 16-byte aligned, nothing to be initialised;
  *              calls that may overlap on the GPU need one each, calls in a row (captured or not) can share one

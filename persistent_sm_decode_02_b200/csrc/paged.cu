@@ -441,10 +441,10 @@ cudaError_t launch_append(const AppendArgs& a, int64_t pages, int units, bool sp
 // byte permute a word.  The weights, in the accumulator's layout, become the second MMA's operand by movmatrix.
 //
 // Scales: a tile lies in one page, so K's scale multiplies its scores, and V's enters the exponent: weights are
-// 2^(s + log2 vs - m' + 13), with a running maximum m' of their own, and the sum uses 2^(s - m).  m' moves only when a
-// score is 2^2 above it, so most tiles need no reduction, and weights stay below 2^15, inside fp16.  Down to 2^-27 of the
-// largest they have fp16's 11 bits, and down to 2^-30 a pair has 20; below, one is off by at most 2^-38 of the largest, a pair by
-// 2^-50.
+// 2^(s - m' + log2 vs + 13), with a running maximum m' of their own, and the sum uses 2^(s - m).  m' moves only when a
+// score is 2^2 above it, so most tiles need no reduction, and weights stay below 2^15, inside fp16.  (m' is rounded up, which
+// costs a weight nothing but range: for scores of 2^28, 2^16 of it.)  Down to 2^-27 of the largest they have fp16's 11 bits,
+// and down to 2^-30 a pair has 20; below, one is off by at most 2^-38 of the largest, a pair by 2^-50.
 // A maximum of -infinity means that no position was seen; one of the lowest finite value, that every score seen was
 // -infinity (those weigh nothing beside a finite score, and alone they have no softmax).
 //
@@ -817,14 +817,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
       const float least = in0 ? -FLT_MAX : -INFINITY;
       const float x0 = fmaxf(fmaxf(in0 ? s0 : least, in1 ? s2 : least), least);
       const float x1 = fmaxf(fmaxf(in0 ? s1 : least, in1 ? s3 : least), least);
-      if (__any_sync(0xffffffffu, x0 > m0 + kGrow || x0 + lv > n0 + kGrow || x1 > m1 + kGrow || x1 + lv > n1 + kGrow)) {
+      const float grow = kGrow - lv;
+      if (__any_sync(0xffffffffu, x0 > m0 + kGrow || x0 - n0 > grow || x1 > m1 + kGrow || x1 - n1 > grow)) {
         float y0 = x0, y1 = x1;
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) {
           y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, w));
           y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, w));
         }
-        const float a0 = fmaxf(m0, y0), a1 = fmaxf(m1, y1), b0 = fmaxf(n0, y0 + lv), b1 = fmaxf(n1, y1 + lv);
+        const float a0 = fmaxf(m0, y0), a1 = fmaxf(m1, y1), b0 = fmaxf(n0, __fadd_ru(y0, lv)), b1 = fmaxf(n1, __fadd_ru(y1, lv));
         l0 *= join_weight(m0, a0);
         l1 *= join_weight(m1, a1);
         const float w0 = join_weight(n0, b0), w1 = join_weight(n1, b1);
@@ -832,9 +833,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(PagedArgs a) {
         for (int i = 0; i < kSteps; ++i) o[i][0] *= w0, o[i][1] *= w1, o[i][2] *= w0, o[i][3] *= w1;
         m0 = a0, m1 = a1, n0 = b0, n1 = b1;
       }
-      const float b0 = lv + kTop - (n0 == -INFINITY ? 0.f : n0), b1 = lv + kTop - (n1 == -INFINITY ? 0.f : n1);
-      const float p0 = in0 ? ex2(s0 + b0) : 0.f, p1 = in0 ? ex2(s1 + b1) : 0.f;
-      const float p2 = in1 ? ex2(s2 + b0) : 0.f, p3 = in1 ? ex2(s3 + b1) : 0.f;
+      // (differences of scores first: they are exact where they matter)
+      const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1, top = lv + kTop;
+      const float p0 = in0 ? ex2(s0 - b0 + top) : 0.f, p1 = in0 ? ex2(s1 - b1 + top) : 0.f;
+      const float p2 = in1 ? ex2(s2 - b0 + top) : 0.f, p3 = in1 ? ex2(s3 - b1 + top) : 0.f;
       l0 += (in0 ? ex2(s0 - m0) : 0.f) + (in1 ? ex2(s2 - m0) : 0.f);
       l1 += (in0 ? ex2(s1 - m1) : 0.f) + (in1 ? ex2(s3 - m1) : 0.f);
       const uint32_t h0 = pack_half(p0, p1), h1 = pack_half(p2, p3);

@@ -204,6 +204,35 @@ def test_paged_scores_that_overflow_weigh_nothing(n, first, dtype):
     assert bool(((out[1].double() - ref).abs() <= DT[dtype][2] * ref.abs() + a * (2.0 ** -20 + n * U)).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e6, 1e7])
+@pytest.mark.parametrize("n,d", [(70, 64), (900, 128), (9000, 64)])
+def test_paged_scores_of_large_size(n, d, size, dtype):
+    """Keys along one direction, V's scales of all sizes: the longest key has all the weight, and its value is the result,
+    rounded once (besides 2^-20, and fp16's 2^-11 for bf16, of the weight)."""
+    h, hkv, ps = 4, 2, 16
+    g = gen(271)
+    lens = [n] * 4
+    pool = Pool(lens, hkv, d, ps, 272).fill(lens, 273)
+    sign = torch.randint(0, 2, (d,), generator=g, device="cuda") * 2.0 - 1.0
+    best = [0, 20, n // 2, n - 1]
+    for b, t in enumerate(best):
+        length = torch.full((len(pool.table[b]) * ps,), 0.25, device="cuda")
+        length[1::3] = 0.5
+        length[t] = 1.0
+        codes = (length[:, None] * sign).to(torch.float8_e4m3fn).view(torch.uint8).view(-1, 1, ps, d)
+        pool.k[pool.table[b].long()] = codes.expand(-1, hkv, -1, -1)
+    pool.ks[pool.table.long()] = 1.0
+    q = (size * sign).expand(4, h, d).to(DT[dtype][0]).contiguous()
+    out = torch.empty_like(q)
+    run_paged(pool, q, out, lens, dtype)
+    for b, t in enumerate(best):
+        _, v = pool.rows(b, n)
+        ref = v[:, t].repeat_interleave(h // hkv, 0)
+        tol = (DT[dtype][2] + 2.0 ** -20 + (2.0 ** -11 if dtype == "bf16" else 0.0)) * ref.abs()
+        assert bool(((out[b].double() - ref).abs() <= tol).all()), b
+
+
 def test_paged_no_page_to_read_gives_zeros():
     """A sequence whose every page id is bad has no position to see."""
     h, hkv, d, ps, lens = 4, 2, 64, 16, [40, 700]
