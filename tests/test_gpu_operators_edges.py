@@ -413,3 +413,72 @@ def test_append_key_codes_are_the_nearest(dtype, d, ps):
         sure = (gap > 2.0 ** -22 * z) | (y == k[lo:hi].transpose(0, 1) / s)
         assert float(sure.double().mean()) > 0.99
         assert torch.equal(torch.where(sure, have, 0.0), torch.where(sure, ops.e4m3_64(y), 0.0))
+
+
+# ------------------------------------------------------------------------------------------------ streams and graphs
+def test_prefill_on_several_streams_at_once():
+    """Calls of both head sizes and types under way together: the bits of each alone."""
+    sets = [("bf16", 64, [900, 30, 700]), ("bf16", 128, [1500, 400]), ("f32", 64, [300, 200]), ("bf16", 64, [64] * 40)]
+    args, want, out = [], [], []
+    for i, (dtype, d, lens) in enumerate(sets):
+        args.append(ops.prefill_inputs(8, 4, d, sum(lens), sum(lens), dtype, 280 + i))
+        want.append(torch.empty_like(args[i][0]))
+        out.append(torch.empty_like(args[i][0]))
+        run_prefill(*args[i], want[i], lens, lens, dtype)
+    cu = [ints(offsets(s[2])) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(15):
+        for i, (dtype, d, lens) in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                run_prefill(*args[i], out[i], cu[i], cu[i], dtype, max_q=max(lens))
+    torch.cuda.synchronize()
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d,ps", [(64, 16), (128, 64)])
+def test_prompts_in_a_captured_graph(d, ps):
+    """Append and prompt attention captured together and replayed on other values and other lengths: the bits of the same calls
+    outside a graph."""
+    h, hkv, total = 8, 2, 700
+    lens = [[400, 1, 299], [17, 683, 0], [233, 233, 234]]
+    fr = ops.freqs(d)
+    x = (torch.randn(3, total, (h + 2 * hkv) * d, generator=gen(290), device="cuda") * 1.28).bfloat16()
+    row, e = x.stride(1), 2
+
+    def once(pool, xin, cu, at, q, k, out):
+        p = xin.data_ptr()
+        st = ops.stream()
+        pool.cache().append(p, p + h * d * e, p + (h + hkv) * d * e, q.data_ptr(), cu.data_ptr(), at.data_ptr(),
+                            pool.table.data_ptr(), table_stride=pool.width, n_seqs=3, n_tokens=total, max_new=total,
+                            n_heads=h, strides=(row, row, row, h * d), inv_freq=fr.data_ptr(), rot_dim=d,
+                            k_out=k.data_ptr(), stream=st)
+        pkg.attention_prefill(q.data_ptr(), k.data_ptr(), p + (h + hkv) * d * e, out.data_ptr(), cu.data_ptr(),
+                              cu.data_ptr(), n_seqs=3, n_q=total, n_k=total, max_q=total, n_heads=h, n_kv_heads=hkv,
+                              head_dim=d, strides=(h * d, hkv * d, row, h * d), stream=st)
+
+    def buffers():
+        pool = Pool([total] * 3, hkv, d, ps, 291)
+        q = torch.empty(total, h, d, dtype=torch.bfloat16, device="cuda")
+        return pool, q, torch.empty(total, hkv, d, dtype=q.dtype, device="cuda"), torch.empty_like(q)
+
+    pool, q, k, out = buffers()
+    xin, cu, at = x[0].clone(), ints(offsets(lens[0])), ints(lens[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        once(pool, xin, cu, at, q, k, out)
+    for i in range(3):
+        xin.copy_(x[i])
+        cu.copy_(ints(offsets(lens[i])))
+        at.copy_(ints(lens[i]))
+        before = pool.state()
+        graph.replay()
+        torch.cuda.synchronize()
+        p2, q2, k2, out2 = buffers()
+        p2.k, p2.v, p2.ks, p2.vs = before
+        once(p2, x[i], ints(offsets(lens[i])), ints(lens[i]), q2, k2, out2)
+        torch.cuda.synchronize()
+        for a, b in ((q, q2), (k, k2), (out, out2), (pool.k, p2.k), (pool.v, p2.v), (pool.ks.nan_to_num(-5.0), p2.ks.nan_to_num(-5.0))):
+            assert torch.equal(a, b), i
