@@ -326,7 +326,10 @@ int dec_attention_noalloc(const float* q, const void* k_cache, const void* v_cac
  * token's; a token's heads lie one behind the other.
  *
  * dtype: DEC_BF16 or DEC_F32, the type of q, k, v and out.  Sums, softmax
- * statistics and rotations are fp32 or better; results are rounded once.
+ * statistics and rotations are fp32 or better; results are rounded once.  A softmax's
+ * weights are rounded before they meet the values: dec_attention_prefill to bf16 for
+ * DEC_BF16 (not for DEC_F32), dec_attention_paged to fp16 for DEC_BF16 and to 20 bits
+ * for DEC_F32 (weights below 2^-27 and 2^-30 of the largest to fewer).
  * Limits (DEC_ERR_UNSUPPORTED otherwise): head_dim 64 or 128, n_heads a multiple of
  * n_kv_heads with at most 8 query heads per kv head (query head h reads kv head
  * h / (n_heads / n_kv_heads)); and sizes whose parts are counted in 32 bits:

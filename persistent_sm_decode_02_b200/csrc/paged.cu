@@ -180,7 +180,7 @@ __device__ __forceinline__ void angles(const AppendArgs& a, int c, int64_t pos, 
 
 // Blocks of a (sequence, page it touches): some for its kv heads, some for its query heads.  A thread holds the same 16
 // dims of its rows for every head, so it computes their 8 angles once.  Bound by memory where tokens are many (4 x 8192
-// tokens, 32 / 8 heads of 128, bf16: 738 MB in 142 us, 5.2 TB/s), by the chain of dependent loads (offsets, page id,
+// tokens, 32 / 8 heads of 128, bf16: 738 MB in 143-148 us, 5.0-5.2 TB/s), by the chain of dependent loads (offsets, page id,
 // row) where they are few (one token 4.0 us).  A page's scale needs all of its new values, so its keys and values stay in
 // registers between the maximum and the rounding and are read once; the next head's are on their way meanwhile.
 template <typename T, int D, int NIT, int ROLE>
@@ -448,15 +448,18 @@ cudaError_t launch_append(const AppendArgs& a, int64_t pages, int units, bool sp
 // A maximum of -infinity means that no position was seen; one of the lowest finite value, that every score seen was
 // -infinity (those weigh nothing beside a finite score, and alone they have no softmax).
 //
-// Bound by memory for large batches: 128 sequences of up to 8192, 32 / 8 heads of 128, 1.26 GB in 221-230 us, 5.5-5.7 TB/s (85 %
-// of the measured copy; blocks with equal work end between 185 and 230 us, as the SMs' shares of the bandwidth differ).
+// Bound by memory for large batches: 128 sequences of up to 8192, 32 / 8 heads of 128, 1.26 GB in 222-227 us, 5.5-5.7 TB/s (85 %
+// of the measured copy), in a graph's calls in a row, 239 us (5.3 TB/s, 80 %) in calls among others; blocks with equal work end
+// between 185 and 230 us, as the SMs' shares of the bandwidth differ.
 // Every warp has three tiles' copies under way, which covers the latency without a barrier between warps.  Small calls are
-// latency: 7.2 us for one sequence of 77, 16.4 us for one of 8193, of which 2-3 us find the place on the line and as much
+// latency: 7.1 us for one sequence of 77, 16.2 us for one of 8193, of which 2-3 us find the place on the line and as much
 // joins; a third of a small call's stalls are first fetches of instructions, so what runs once is kept short.
 constexpr int kBlocks = 148;  // one block per SM of a B200
 constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
-constexpr int kLeast = 2;   // tiles a warp has at least before another block is taken (1, 2, 4: 8193 positions 20.3, 20.3, 21.9 us)
+// tiles a warp has at least before another block is taken (1, 2, 4: 77 positions 8.1, 7.0, 7.6 us; 512 12.3, 12.8, 14.3; 8193
+// 16.3, 16.2, 17.2)
+constexpr int kLeast = 2;
 
 struct PagedArgs {
   Cache c;
@@ -1149,8 +1152,8 @@ extern "C" int dec_kv_append(const dec_paged_cache* cache, const dec_rope* rope,
   // A block a kv head, and one for its query heads, is the shortest path for few tokens; more blocks than fill the GPU
   // compute the angles over and over.  With blocks that a page fills (256 threads or more) twice the SMs are enough
   // and queries and keys are launches of their own, each with the registers it needs; with little in each, 8 an SM.  B200,
-  // 32 / 8 heads of 128, us, one way and the other: 256 single tokens 7.1 (8 an SM) / 9.9 (2), 8 x 1000 tokens 50.3 / 41.6,
-  // 4 x 8192 154 (one launch) / 138 (two), 64 x 4 tokens 5.0 / 9.8.
+  // 32 / 8 heads of 128, bf16, us, one way and the other: 256 single tokens 7.4 (8 an SM) / 11.1 (2), 64 x 4 5.5 / 7.0, 8 x 1000
+  // 51.8 / 43.2, 4 x 8192 158 (one launch) / 143 (two).
   const bool split = q && units >= 256;
   const int64_t enough = split ? 2 * 148 : 8 * 148;
   // (a block notes borders in shared memory: 128 bytes a head, which is enough for 128 heads)

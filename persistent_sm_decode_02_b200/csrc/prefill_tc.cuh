@@ -13,8 +13,8 @@
 // and once it has arrived O_i is at rest until the tile's next P: a softmax thread may rescale its row of O there.  It
 // does only when the row's maximum has grown by more than 2^8 (P up to 2^8 and its sum lose nothing).
 //
-// P is rounded to bf16 (2^-9 of each weight, of the same size as V's own rounding and the result's); its sum is
-// of the unrounded weights, in fp32.
+// P is rounded to bf16 (by up to 2^-8 of each weight, as much as V's own rounding and the result's: the two operands of an MMA
+// have one type, and V in two parts would double the P V); its sum is of the unrounded weights, in fp32.
 //
 // An unseen value meets a weight of zero, and zero times NaN or infinity is NaN.  Values behind a sequence's last key (another
 // sequence's, or nobody's) are zeroed in shared memory before P V of the step that holds it.  (To cut that P V short at the
@@ -23,11 +23,12 @@
 // result is not finite although every value that the row sees in that dim is, the row is computed once more with the keys it
 // sees alone.  That takes a warp long where keys are many; the block's other warps wait for it as long as it gets on.
 //
-// What it measures: a causal 8k prompt, 32 heads of 128 on 8, 440-465 us, 1.18-1.25 PFLOP/s (72-76 % of cuBLAS's burst
-// rate); of heads of 64 325 us.  With the softmax left out the MMAs, loads and hand-overs take 395 us: the tensor cores wait
-// for hand-overs (about 800 cycles from S to P and on, two tiles to hide them) and for shared memory (Q K^T reads both
-// operands there at its full 128 bytes a cycle).  Tried and slower: two threads a row (115 against 100 us for six ragged
-// prompts of up to 1500, heads of 64; spills at 128), steps of 64 keys with two S buffers for heads of 128 (543).
+// What it measures: a causal 8k prompt, 32 heads of 128 on 8, 437-497 us, 1.11-1.26 PFLOP/s (67-77 % of cuBLAS's burst
+// rate), and 512 us in calls among others for seconds, under the power cap (78 % of its sustained rate); of heads of 64
+// 320-343.  With the softmax left out the MMAs, loads and hand-overs of heads of 128 take 395 us: the tensor cores wait for
+// hand-overs (about 800 cycles from S to P and on, two tiles to hide them) and for shared memory (Q K^T reads both operands
+// there at its full 128 bytes a cycle).  Tried and slower: two threads a row (115 against 100 us for six ragged prompts of up
+// to 1500, heads of 64; spills at 128), steps of 64 keys with two S buffers for heads of 128 (543).
 #pragma once
 #include <cuda.h>
 
@@ -73,7 +74,7 @@ struct Tiling {
 };
 inline Tiling tiling(int n_seqs, int n_q, int max_q, int rows) {
   const int64_t each = ((int64_t)max_q + rows - 1) / rows, batch = (int64_t)n_q / rows + n_seqs;
-  // 8 prompts of 4096 among 500 of up to 100, 32 heads of 128: 1.39 ms packed, 1.63 with 32 tiles for each; of 64: 1.29, 2.97.
+  // 8 prompts of 4096 among 500 of up to 100, 32 heads of 128: 1.35 ms packed, 1.63 with 32 tiles for each; of 64: 1.28, 2.85.
   // Of about one length, the plain cut's order (longest rows of all sequences first) ends more evenly.
   return n_seqs * each > 4 * batch ? Tiling{(int)batch, 1} : Tiling{(int)each, 0};
 }
@@ -110,7 +111,7 @@ using dec::smem_u32;
 
 constexpr int kM = 128;
 // Of every 8 pairs of a row's exponentials, those that the polynomial does.  8k causal prompt, 32 heads, us for 0 / 2 / 3 / 4:
-// heads of 128 492 / 465 / 469 / 530, of 64 337 / 325 / 328 / 362.
+// heads of 128 491 / 461 / 502 / 507, of 64 351 / 335 / 333 / 362.
 constexpr int kPoly = 2;
 constexpr float kC0 = 0x1.fff692p-1f, kC1 = 0x1.62f31ap-1f, kC2 = 0x1.f0de1ap-3f, kC3 = 0x1.c3f75ep-5f;
 
@@ -119,7 +120,7 @@ constexpr float kHuge = 0x1p26f;
 // Heads of 128: S and O of two tiles with steps of 128 keys fill an SM's TMEM, one block has the SM to itself, and its
 // softmax threads keep a row of S in registers that they take over from the last warpgroup.  The block stays: warp 10 asks
 // for the work of blocks that have not begun, and while the softmax warps write one pair of tiles the next one's loads and
-// Q K^T are under way (16 ragged prompts of up to 512: 52 us, a block for each pair 64; one of 8192: 440 / 448).
+// Q K^T are under way (with a block for each pair 16 ragged prompts of up to 512 took 23 % longer, one of 8192 2 %).
 // Heads of 64: with steps of 64 keys they fill half of it, and two blocks share an SM (shared memory lets no third in):
 // four tiles whose waits overlap, as do one block's first loads and last stores with the other's steps.
 template <int D>

@@ -415,6 +415,18 @@ def test_append_key_codes_are_the_nearest(dtype, d, ps):
         assert torch.equal(torch.where(sure, have, 0.0), torch.where(sure, ops.e4m3_64(y), 0.0))
 
 
+@pytest.mark.parametrize("h,hkv,d,ps,old,new", [(160, 160, 64, 16, 5, [90] * 24), (300, 150, 64, 128, 0, [500, 3, 260]),
+                                                (129, 129, 128, 16, 30, [1] * 40)])
+def test_append_more_kv_heads_than_a_block_takes(h, hkv, d, ps, old, new):
+    old = [old] * len(new)
+    pool = Pool([a + b for a, b in zip(old, new)], hkv, d, ps, 295).fill(old, 296)
+    x = torch.randn(sum(new), (h + 2 * hkv) * d, generator=gen(297), device="cuda")
+    q_out = torch.empty(sum(new), h, d, device="cuda")
+    before = pool.state()
+    run_append(pool, x, q_out, h, new, [a + b for a, b in zip(old, new)], ops.freqs(d), "half", "f32")
+    ops.check_append(pool, before, x, q_out, h, old, new, ops.freqs(d), "half", "f32")
+
+
 # ------------------------------------------------------------------------------------------------ streams and graphs
 def test_prefill_on_several_streams_at_once():
     """Calls of both head sizes and types under way together: the bits of each alone."""
